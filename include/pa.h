@@ -101,7 +101,7 @@ typedef enum pa_status {
     PA_ERR_NOT_FOUND = 7      /* unknown sequence id (host block manager) */
 } pa_status;
 
-typedef enum pa_dtype { PA_F32 = 0, PA_BF16 = 1, PA_FP8_E4M3 = 2 } pa_dtype;
+typedef enum pa_dtype { PA_F32 = 0, PA_BF16 = 1, PA_FP8_E4M3 = 2, PA_INT8 = 3 } pa_dtype;
 
 /* Bits a kernel ORs into *err_flag. */
 #define PA_DEVERR_BLOCK_ID 1     /* block table entry outside [0, num_blocks) */
@@ -110,6 +110,7 @@ typedef enum pa_dtype { PA_F32 = 0, PA_BF16 = 1, PA_FP8_E4M3 = 2 } pa_dtype;
 #define PA_DEVERR_PAIR 8         /* copy pair id outside [0, num_blocks) */
 #define PA_DEVERR_TIMEOUT 16     /* a bounded in-kernel wait ran out */
 #define PA_DEVERR_CHUNK 32       /* chunk_len < 0, > max_chunk or > context_len */
+#define PA_DEVERR_PLAN 64        /* a step does not fit: lengths, tables, slots or free blocks */
 
 /* The KV pool one call works on. */
 typedef struct pa_cache_desc {
@@ -313,6 +314,114 @@ PA_API pa_status pa_prefill_chunk(const void *query, const void *key_cache, cons
                            int32_t num_seqs, int32_t max_chunk, int32_t num_q_heads, float scale,
                            void *out, const pa_cache_desc *cache, int32_t *err_flag,
                            void *stream);
+
+/*
+ * One step's block tables, slot mapping and sequence starts, built on the GPU from
+ * the requests' lengths: pa_bm_append_step for callers that keep tables, lengths and
+ * free blocks on the device (no copy to or from the host, replayable from a graph).
+ * Sequence s holds context_lens[s] tokens in the first ceil(context_lens[s] / 16)
+ * entries of its table and appends counts[s] >= 0.  The blocks it lacks are popped
+ * from free_blocks[0 .. *num_free), last entry first, sequence by sequence:
+ *   block_tables[s][ceil(len / 16) ..] get the popped ids (other entries are kept),
+ *   slot_mapping[i], for the i-th appended token of the step (sequence by sequence),
+ *     = block * 16 + offset of its position; entries behind the last token become -1
+ *     (padding, as the cache writes take it), up to slot_capacity,
+ *   seq_starts[0 .. num_seqs] = where each sequence's tokens start (the exclusive sums
+ *     of counts, then their total) -- also what pa_prefill_packed takes,
+ *   new_context_lens[s] = len + count, *new_num_free = *num_free - blocks popped.
+ * new_context_lens may be context_lens and new_num_free may be num_free (the step in
+ * place); otherwise outputs and inputs must not overlap.  Sequences that share blocks
+ * (forks) need the host manager's copy on write before they append.
+ * All or nothing: a negative count or length, a table row, slot_mapping or the free
+ * stack too short, or *num_free outside [0, free_capacity] sets PA_DEVERR_PLAN, and
+ * then tables, lengths and stack height stay as they were (copied to the new ones),
+ * every slot is -1 and every start 0.  Ids on the stack are not checked here (the
+ * calls that use them do); a negative id gives slot -1 and PA_DEVERR_BLOCK_ID.
+ * num_seqs <= 16384, slot_capacity <= 2^30.
+ * Source: devpress teardown, 关键设计一 (append_slot takes a block from the free list
+ * when the current one is full); chenxutan 3.3.
+ */
+PA_API pa_status pa_step_plan(const int32_t *counts, const int32_t *context_lens, int32_t num_seqs,
+                              int32_t *block_tables, int32_t max_blocks_per_seq, const int32_t *free_blocks,
+                              int32_t free_capacity, const int32_t *num_free, int64_t *slot_mapping,
+                              int32_t slot_capacity, int32_t *seq_starts, int32_t *new_context_lens,
+                              int32_t *new_num_free, int32_t *err_flag, void *stream);
+
+/*
+ * The return of finished sequences' blocks to pa_step_plan's stack: for every s with
+ * finished[s] != 0, in order, its blocks are pushed in logical order (as
+ * pa_bm_free_seq does for blocks nobody shares), their table entries become -1 and
+ * new_context_lens[s] = 0; the other sequences keep theirs.  In place as above; all
+ * or nothing (PA_DEVERR_PLAN) when a length does not fit its table or the stack its
+ * capacity.  A block must be in one table only: blocks shared by a fork belong to
+ * the host manager.
+ */
+PA_API pa_status pa_step_release(const int32_t *finished, const int32_t *context_lens, int32_t num_seqs,
+                                 int32_t *block_tables, int32_t max_blocks_per_seq, int32_t *free_blocks,
+                                 int32_t free_capacity, const int32_t *num_free, int32_t *new_context_lens,
+                                 int32_t *new_num_free, int32_t *err_flag, void *stream);
+
+/*
+ * 8-bit cache with a scale per (block, kv head).  The pools hold one-byte codes in
+ * the layout of the other pools, dtype PA_FP8_E4M3 or PA_INT8 (two's complement, -127
+ * .. 127); key_scales and value_scales are float [num_blocks, num_kv_heads], and a
+ * value is code * scale.  Nothing has to be calibrated: the scale follows the data.
+ * (k_scale and v_scale of the descriptor are not used.)  head_dim 64 or 128; key,
+ * value, query and out are bf16.
+ *
+ * The append: for the tokens of this call that go to block b, kv head h, let A be the
+ * largest |x| over their finite elements, Q = 448 (e4m3) or 127 (int8), and
+ *   need  = the smallest power of two with A <= need * Q, at least 2^-64;
+ *   sigma = max(stored scale, need), or need when slot 0 of the block is among the
+ *           call's (the block starts anew) or the stored scale is no finite positive number.
+ * The tokens' codes are round(x / sigma), nearest even (infinities saturate; NaN is
+ * the e4m3 NaN, or 0 in int8).  Where sigma is larger than the stored scale, the codes
+ * of the block's other slots in front of the last one written become round(code *
+ * stored / sigma).  Slots behind it, and all other blocks, are left as they are.
+ * sigma is stored.  Powers of two make both roundings exact up to that one rounding.
+ * key and value: [num_tokens, num_kv_heads, head_dim], a token's heads and dims
+ * contiguous, tokens key_stride / value_stride elements apart (at least num_kv_heads *
+ * head_dim, a multiple of 8), so that they can be views of one fused projection.
+ * Slots as in pa_cache_write.  The tokens of one block must stand next to each other
+ * in slot_mapping, as pa_bm_append_step and pa_step_plan put them (in any order, with
+ * no padding in between); a block whose tokens stand in two places gets an unspecified
+ * scale and codes.  Two tokens with the same slot: unspecified which one lands.
+ * Scales need no initial value.
+ * Source: chenxutan 5.3 (8-bit KV); devpress architecture figure (FP8/INT8).
+ */
+PA_API pa_status pa_cache_write_scaled(const void *key, const void *value, int64_t key_stride,
+                                       int64_t value_stride, const int64_t *slot_mapping, int32_t num_tokens,
+                                       void *key_cache, void *value_cache, float *key_scales,
+                                       float *value_scales, const pa_cache_desc *cache, int32_t *err_flag,
+                                       void *stream);
+
+/* pa_copy_blocks for such pools: codes and scales of every pair's block. */
+PA_API pa_status pa_copy_blocks_scaled(void *key_cache, void *value_cache, float *key_scales,
+                                       float *value_scales, const int32_t *src_dst_pairs, int32_t num_pairs,
+                                       const pa_cache_desc *cache, int32_t *err_flag, void *stream);
+
+/* Bytes of workspace pa_decode_scaled needs: it depends on the heads only, not on the
+ * number or length of the contexts.  0 for head counts that do not divide. */
+PA_API size_t pa_decode_scaled_workspace_size(int32_t num_q_heads, int32_t num_kv_heads, int32_t head_dim);
+
+/*
+ * pa_decode over such pools: one query token per sequence,
+ *   out[s][h][:] = sum_t softmax_t(scale * <query[s][h], K_s[t]>) V_s[t],
+ * K_s[t] = key code * key_scales[block][kv head] (V alike).  Arguments and errors as in
+ * pa_decode; L_s == 0 gives 0.  The context is always split evenly over the GPU; a
+ * sequence's result does not depend on the other sequences beyond the order of fp32
+ * sums.  Two kernels.  The workspace's contents need not be set and mean nothing
+ * afterwards; calls that overlap on the GPU need workspaces of their own.  Replays
+ * correctly from a graph, following context_lens.  num_seqs <= 16384 and
+ * num_seqs * (max_context_len / 16 + 2) < 2^31.  Scores, sums and the accumulator are fp32;
+ * probabilities are rounded to f16 for the product with V, the query is exact in f16.
+ */
+PA_API pa_status pa_decode_scaled(const void *query, const void *key_cache, const void *value_cache,
+                                  const float *key_scales, const float *value_scales,
+                                  const int32_t *block_tables, int32_t max_blocks_per_seq,
+                                  const int32_t *context_lens, int32_t max_context_len, int32_t num_seqs,
+                                  int32_t num_q_heads, float scale, void *workspace, size_t workspace_bytes,
+                                  void *out, const pa_cache_desc *cache, int32_t *err_flag, void *stream);
 
 /*
  * Wait for `stream` to finish (polling, at most timeout_ms milliseconds) and read

@@ -9,6 +9,7 @@ If the shared library is missing the import fails loudly.
 from __future__ import annotations
 
 import ctypes as C
+import functools
 import os
 
 import numpy as np
@@ -18,9 +19,10 @@ LIB_PATH = os.path.join(_HERE, "libpa_b200.so")
 
 PA_OK, PA_ERR_INVALID_ARG, PA_ERR_UNSUPPORTED, PA_ERR_OOM = 0, 1, 2, 3
 PA_ERR_DEVICE_INDEX, PA_ERR_CUDA, PA_ERR_TIMEOUT, PA_ERR_NOT_FOUND = 4, 5, 6, 7
-PA_F32, PA_BF16, PA_FP8_E4M3 = 0, 1, 2
+PA_F32, PA_BF16, PA_FP8_E4M3, PA_INT8 = 0, 1, 2, 3
 PA_DEVERR_BLOCK_ID, PA_DEVERR_SLOT, PA_DEVERR_CONTEXT_LEN = 1, 2, 4
 PA_DEVERR_PAIR, PA_DEVERR_TIMEOUT, PA_DEVERR_CHUNK = 8, 16, 32
+PA_DEVERR_PLAN = 64
 BLOCK_SIZE = 16
 
 
@@ -56,6 +58,12 @@ def _load():
                                        vp, sz, vp, desc, vp, vp]),
         "pa_prefill_chunk": (C.c_int, [vp, vp, vp, vp, i32, vp, vp, i32, i32, i32, f32, vp, desc,
                                        vp, vp]),
+        "pa_step_plan": (C.c_int, [vp, vp, i32, vp, i32, vp, i32, vp, vp, i32, vp, vp, vp, vp, vp]),
+        "pa_step_release": (C.c_int, [vp, vp, i32, vp, i32, vp, i32, vp, vp, vp, vp, vp]),
+        "pa_cache_write_scaled": (C.c_int, [vp, vp, i64, i64, vp, i32, vp, vp, vp, vp, desc, vp, vp]),
+        "pa_copy_blocks_scaled": (C.c_int, [vp, vp, vp, vp, vp, i32, desc, vp, vp]),
+        "pa_decode_scaled_workspace_size": (sz, [i32, i32, i32]),
+        "pa_decode_scaled": (C.c_int, [vp, vp, vp, vp, vp, vp, i32, vp, i32, i32, i32, f32, vp, sz, vp, desc, vp, vp]),
         "pa_wait": (C.c_int, [vp, vp, i32, C.POINTER(i32)]),
         "pa_set_wait_timeout_ns": (C.c_uint64, [C.c_uint64]),
         "pa_bm_create": (C.c_int, [i32, i32, vp, C.POINTER(vp)]),
@@ -96,6 +104,8 @@ _lib = _load()
 EXPORTED = (
     "pa_abi_version", "pa_status_string", "pa_cache_write", "pa_copy_blocks", "pa_check_copy_pairs",
     "pa_decode_workspace_size", "pa_decode_launches", "pa_decode", "pa_append_decode", "pa_prefill_chunk",
+    "pa_step_plan", "pa_step_release", "pa_cache_write_scaled", "pa_copy_blocks_scaled",
+    "pa_decode_scaled_workspace_size", "pa_decode_scaled",
     "pa_wait", "pa_set_wait_timeout_ns",
 )
 
@@ -259,6 +269,175 @@ def pa_prefill_chunk(query, key_cache, value_cache, block_tables, context_lens, 
                                  block_tables.shape[1], _ptr(context_lens), _ptr(chunk_lens), S, mc,
                                  hq, float(scale), _ptr(out), C.byref(d), _ptr(err_flag),
                                  _stream(stream)), "pa_prefill_chunk")
+
+
+# ------------------------------------------------ serving step: plan, 8-bit cache
+# These calls check that every tensor is on one CUDA device and launch there, on `stream`
+# or on that device's current stream.
+def _run(name, dev, stream, *args):
+    """Call the library with the stream appended; the tensors' device is made current."""
+    torch = _torch()
+    fn = getattr(_lib, name)
+    if dev.index == torch.cuda.current_device():
+        st = stream if stream is not None else torch.cuda.current_stream(dev)
+        status = fn(*args, st.cuda_stream)
+    else:
+        with torch.cuda.device(dev):
+            st = stream if stream is not None else torch.cuda.current_stream(dev)
+            status = fn(*args, st.cuda_stream)
+    if status != PA_OK:
+        raise PAError(status, name)
+
+
+def _on_device(*tensors):
+    """The CUDA device all tensors (None skipped) are on."""
+    dev = tensors[0].device
+    assert dev.type == "cuda", "tensors passed to the library must be on a CUDA device"
+    for t in tensors:
+        assert t is None or t.device == dev, "tensors of one call must be on one device"
+    return dev
+
+
+def _check_int(t, dtype, shape, what):
+    assert t.dtype == dtype and t.shape == shape and t.is_contiguous(), \
+        f"{what}: contiguous {dtype} of shape {tuple(shape)} wanted, got {t.dtype} {tuple(t.shape)}"
+
+
+def _addr(t):
+    return None if t is None else t.data_ptr()
+
+
+def pa_step_plan(counts, context_lens, block_tables, free_blocks, num_free, slot_mapping, seq_starts,
+                 new_context_lens=None, new_num_free=None, err_flag=None, stream=None):
+    """Tables, slots and starts of one step on the GPU: append counts[s] tokens to every
+    sequence.  counts, context_lens int32 [S]; block_tables int32 [S, max_blocks] (extended in
+    place); free_blocks int32 [N] with its height num_free int32 [1]; out: slot_mapping int64
+    [capacity], seq_starts int32 [S + 1], new_context_lens and new_num_free (default: in place)."""
+    torch = _torch()
+    i32 = torch.int32
+    new_context_lens = context_lens if new_context_lens is None else new_context_lens
+    new_num_free = num_free if new_num_free is None else new_num_free
+    S = counts.shape[0]
+    _check_int(counts, i32, (S,), "counts")
+    _check_int(context_lens, i32, (S,), "context_lens")
+    _check_int(new_context_lens, i32, (S,), "new_context_lens")
+    _check_int(seq_starts, i32, (S + 1,), "seq_starts")
+    _check_int(num_free, i32, (1,), "num_free")
+    _check_int(new_num_free, i32, (1,), "new_num_free")
+    assert block_tables.dim() == 2 and free_blocks.dim() == 1 and slot_mapping.dim() == 1
+    _check_int(block_tables, i32, (S, block_tables.shape[1]), "block_tables")
+    _check_int(free_blocks, i32, free_blocks.shape, "free_blocks")
+    _check_int(slot_mapping, torch.int64, slot_mapping.shape, "slot_mapping")
+    dev = _on_device(counts, context_lens, block_tables, free_blocks, num_free, slot_mapping, seq_starts,
+                     new_context_lens, new_num_free, err_flag)
+    _run("pa_step_plan", dev, stream, counts.data_ptr(), context_lens.data_ptr(), S, block_tables.data_ptr(),
+         block_tables.shape[1], free_blocks.data_ptr(), free_blocks.shape[0], num_free.data_ptr(),
+         slot_mapping.data_ptr(), slot_mapping.shape[0], seq_starts.data_ptr(), new_context_lens.data_ptr(),
+         new_num_free.data_ptr(), _addr(err_flag))
+
+
+def pa_step_release(finished, context_lens, block_tables, free_blocks, num_free, new_context_lens=None,
+                    new_num_free=None, err_flag=None, stream=None):
+    """Give the blocks of the sequences with finished[s] != 0 (int32 [S]) back to the stack."""
+    torch = _torch()
+    i32 = torch.int32
+    new_context_lens = context_lens if new_context_lens is None else new_context_lens
+    new_num_free = num_free if new_num_free is None else new_num_free
+    S = finished.shape[0]
+    for t, what in ((finished, "finished"), (context_lens, "context_lens"), (new_context_lens, "new_context_lens")):
+        _check_int(t, i32, (S,), what)
+    _check_int(num_free, i32, (1,), "num_free")
+    _check_int(new_num_free, i32, (1,), "new_num_free")
+    assert block_tables.dim() == 2 and free_blocks.dim() == 1
+    _check_int(block_tables, i32, (S, block_tables.shape[1]), "block_tables")
+    _check_int(free_blocks, i32, free_blocks.shape, "free_blocks")
+    dev = _on_device(finished, context_lens, block_tables, free_blocks, num_free, new_context_lens, new_num_free,
+                     err_flag)
+    _run("pa_step_release", dev, stream, finished.data_ptr(), context_lens.data_ptr(), S, block_tables.data_ptr(),
+         block_tables.shape[1], free_blocks.data_ptr(), free_blocks.shape[0], num_free.data_ptr(),
+         new_context_lens.data_ptr(), new_num_free.data_ptr(), _addr(err_flag))
+
+
+@functools.lru_cache(maxsize=64)
+def _scaled_desc(shape, code):
+    return CacheDesc(*shape, code, 1.0, 1.0)
+
+
+def _scaled_pool(key_cache, value_cache, key_scales, value_scales):
+    """Descriptor of pools of torch.float8_e4m3fn or torch.int8 codes with float32 scales
+    [num_blocks, num_kv_heads]."""
+    torch = _torch()
+    dt = key_cache.dtype
+    if dt == torch.float8_e4m3fn:
+        code = PA_FP8_E4M3
+    elif dt == torch.int8:
+        code = PA_INT8
+    else:
+        raise TypeError(f"unsupported dtype {dt}")
+    shape = key_cache.shape
+    assert value_cache.dtype == dt and value_cache.shape == shape and len(shape) == 4
+    assert key_cache.is_contiguous() and value_cache.is_contiguous()
+    _check_int(key_scales, torch.float32, shape[:2], "key_scales")
+    _check_int(value_scales, torch.float32, shape[:2], "value_scales")
+    return C.byref(_scaled_desc(tuple(shape), code))
+
+
+def _token_rows(t, heads, d, what):
+    """Elements between tokens of a [T, heads, d] tensor whose heads and dims are contiguous."""
+    assert t.dim() == 3 and t.shape[1] == heads and t.shape[2] == d, f"{what}: [T, {heads}, {d}] wanted"
+    assert t.stride(2) == 1 and (heads == 1 or t.stride(1) == d), f"{what}: heads and dims must be contiguous"
+    return t.stride(0) if t.shape[0] > 1 else heads * d
+
+
+def pa_cache_write_scaled(key, value, slot_mapping, key_cache, value_cache, key_scales, value_scales,
+                          err_flag=None, stream=None):
+    """Append key/value bf16 [T, Hkv, d] (tokens may be strided) at slot_mapping (int64 [T]) to
+    8-bit pools with a power-of-two scale per (block, kv head)."""
+    torch = _torch()
+    d = _scaled_pool(key_cache, value_cache, key_scales, value_scales)
+    T, hkv, hd = key.shape[0], key_cache.shape[1], key_cache.shape[3]
+    assert key.dtype == torch.bfloat16 == value.dtype and value.shape[0] == T
+    ks, vs = _token_rows(key, hkv, hd, "key"), _token_rows(value, hkv, hd, "value")
+    _check_int(slot_mapping, torch.int64, (T,), "slot_mapping")
+    dev = _on_device(key, value, slot_mapping, key_cache, value_cache, key_scales, value_scales, err_flag)
+    _run("pa_cache_write_scaled", dev, stream, key.data_ptr(), value.data_ptr(), ks, vs, slot_mapping.data_ptr(), T,
+         key_cache.data_ptr(), value_cache.data_ptr(), key_scales.data_ptr(), value_scales.data_ptr(), d,
+         _addr(err_flag))
+
+
+def pa_copy_blocks_scaled(key_cache, value_cache, key_scales, value_scales, src_dst_pairs, err_flag=None, stream=None):
+    """Copy whole blocks, codes and scales, src -> dst for each row of int32 [P, 2]."""
+    torch = _torch()
+    d = _scaled_pool(key_cache, value_cache, key_scales, value_scales)
+    assert src_dst_pairs.dim() == 2
+    _check_int(src_dst_pairs, torch.int32, (src_dst_pairs.shape[0], 2), "src_dst_pairs")
+    dev = _on_device(key_cache, value_cache, key_scales, value_scales, src_dst_pairs, err_flag)
+    _run("pa_copy_blocks_scaled", dev, stream, key_cache.data_ptr(), value_cache.data_ptr(), key_scales.data_ptr(),
+         value_scales.data_ptr(), src_dst_pairs.data_ptr(), src_dst_pairs.shape[0], d, _addr(err_flag))
+
+
+def pa_decode_scaled_workspace_size(num_q_heads, num_kv_heads, head_dim) -> int:
+    return int(_lib.pa_decode_scaled_workspace_size(num_q_heads, num_kv_heads, head_dim))
+
+
+def pa_decode_scaled(query, key_cache, value_cache, key_scales, value_scales, block_tables, context_lens,
+                     max_context_len, scale, out, workspace, err_flag=None, stream=None):
+    """Decode attention over 8-bit pools with a scale per (block, kv head); query/out bf16
+    [S, Hq, d]; workspace of pa_decode_scaled_workspace_size(Hq, Hkv, d) bytes."""
+    torch = _torch()
+    d = _scaled_pool(key_cache, value_cache, key_scales, value_scales)
+    S, hq, hd = query.shape
+    assert query.dtype == torch.bfloat16 == out.dtype and out.shape == query.shape and hd == key_cache.shape[3]
+    assert query.is_contiguous() and out.is_contiguous() and workspace.is_contiguous()
+    assert block_tables.dim() == 2
+    _check_int(block_tables, torch.int32, (S, block_tables.shape[1]), "block_tables")
+    _check_int(context_lens, torch.int32, (S,), "context_lens")
+    dev = _on_device(query, key_cache, value_cache, key_scales, value_scales, block_tables, context_lens, out, workspace,
+                     err_flag)
+    _run("pa_decode_scaled", dev, stream, query.data_ptr(), key_cache.data_ptr(), value_cache.data_ptr(),
+         key_scales.data_ptr(), value_scales.data_ptr(), block_tables.data_ptr(), block_tables.shape[1],
+         context_lens.data_ptr(), int(max_context_len), S, hq, float(scale), workspace.data_ptr(),
+         workspace.numel() * workspace.element_size(), out.data_ptr(), d, _addr(err_flag))
 
 
 def pa_wait(err_flag=None, stream=None, timeout_ms: int = 10000) -> int:

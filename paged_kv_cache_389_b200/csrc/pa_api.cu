@@ -10,6 +10,7 @@
 #include "pa_trace.h"
 #include "pa_common.cuh"
 #include "pa_launch.h"
+#include "pa_step.h"
 
 namespace pa {
 
@@ -309,6 +310,140 @@ pa_status pa_prefill_chunk(const void *query, const void *key_cache, const void 
     const cudaError_t e = launch_prefill(a, static_cast<cudaStream_t>(stream));
     if (e == cudaErrorNotSupported) return PA_ERR_UNSUPPORTED;
     return from_cuda(e);
+}
+
+pa_status pa_step_plan(const int32_t *counts, const int32_t *context_lens, int32_t num_seqs,
+                       int32_t *block_tables, int32_t max_blocks_per_seq, const int32_t *free_blocks,
+                       int32_t free_capacity, const int32_t *num_free, int64_t *slot_mapping,
+                       int32_t slot_capacity, int32_t *seq_starts, int32_t *new_context_lens,
+                       int32_t *new_num_free, int32_t *err_flag, void *stream) {
+    const NvtxRange nvtx_range("pa_step_plan");
+    if (num_seqs < 0 || max_blocks_per_seq < 0 || free_capacity < 0 || slot_capacity < 0)
+        return PA_ERR_INVALID_ARG;
+    if (num_seqs > kMaxPlanSeqs || slot_capacity > (1 << 30)) return PA_ERR_UNSUPPORTED;
+    if (!num_free || !new_num_free || !seq_starts) return PA_ERR_INVALID_ARG;
+    if (num_seqs > 0 && (!counts || !context_lens || !new_context_lens)) return PA_ERR_INVALID_ARG;
+    if (num_seqs > 0 && max_blocks_per_seq > 0 && !block_tables) return PA_ERR_INVALID_ARG;
+    if ((free_capacity > 0 && !free_blocks) || (slot_capacity > 0 && !slot_mapping)) return PA_ERR_INVALID_ARG;
+    const StepPlan p{counts, context_lens, num_seqs, block_tables, max_blocks_per_seq, free_blocks, nullptr,
+                     free_capacity, num_free, slot_mapping, slot_capacity, seq_starts, new_context_lens,
+                     new_num_free, err_flag};
+    return from_cuda(launch_step_plan(p, false, static_cast<cudaStream_t>(stream)));
+}
+
+pa_status pa_step_release(const int32_t *finished, const int32_t *context_lens, int32_t num_seqs,
+                          int32_t *block_tables, int32_t max_blocks_per_seq, int32_t *free_blocks,
+                          int32_t free_capacity, const int32_t *num_free, int32_t *new_context_lens,
+                          int32_t *new_num_free, int32_t *err_flag, void *stream) {
+    const NvtxRange nvtx_range("pa_step_release");
+    if (num_seqs < 0 || max_blocks_per_seq < 0 || free_capacity < 0) return PA_ERR_INVALID_ARG;
+    if (num_seqs > kMaxPlanSeqs) return PA_ERR_UNSUPPORTED;
+    if (!num_free || !new_num_free) return PA_ERR_INVALID_ARG;
+    if (num_seqs > 0 && (!finished || !context_lens || !new_context_lens)) return PA_ERR_INVALID_ARG;
+    if (num_seqs > 0 && max_blocks_per_seq > 0 && !block_tables) return PA_ERR_INVALID_ARG;
+    if (free_capacity > 0 && !free_blocks) return PA_ERR_INVALID_ARG;
+    const StepPlan p{finished, context_lens, num_seqs, block_tables, max_blocks_per_seq, free_blocks, free_blocks,
+                     free_capacity, num_free, nullptr, 0, nullptr, new_context_lens, new_num_free, err_flag};
+    return from_cuda(launch_step_plan(p, true, static_cast<cudaStream_t>(stream)));
+}
+
+namespace {
+// The pool of an 8-bit cache with a scale per (block, kv head).
+pa_status check_scaled(const void *key_cache, const void *value_cache, const float *key_scales,
+                       const float *value_scales, const pa_cache_desc *c, ScaledPool &pool) {
+    if (!c) return PA_ERR_INVALID_ARG;
+    if (c->num_blocks < 0 || c->num_kv_heads <= 0) return PA_ERR_INVALID_ARG;
+    if (c->block_size != kBlockSize) return PA_ERR_UNSUPPORTED;
+    if (c->head_dim != 64 && c->head_dim != 128) return PA_ERR_UNSUPPORTED;
+    if (c->dtype != PA_FP8_E4M3 && c->dtype != PA_INT8) return PA_ERR_UNSUPPORTED;
+    if (!key_cache || !value_cache || !key_scales || !value_scales) return PA_ERR_INVALID_ARG;
+    if (!aligned16(key_cache) || !aligned16(value_cache)) return PA_ERR_INVALID_ARG;
+    if ((reinterpret_cast<uintptr_t>(key_scales) | reinterpret_cast<uintptr_t>(value_scales)) & 3u)
+        return PA_ERR_INVALID_ARG;
+    pool = ScaledPool{const_cast<void *>(key_cache), const_cast<void *>(value_cache), const_cast<float *>(key_scales),
+                      const_cast<float *>(value_scales), c->num_blocks, c->num_kv_heads, c->head_dim,
+                      c->dtype == PA_INT8};
+    return PA_OK;
+}
+}  // namespace
+
+pa_status pa_cache_write_scaled(const void *key, const void *value, int64_t key_stride, int64_t value_stride,
+                                const int64_t *slot_mapping, int32_t num_tokens, void *key_cache,
+                                void *value_cache, float *key_scales, float *value_scales,
+                                const pa_cache_desc *cache, int32_t *err_flag, void *stream) {
+    const NvtxRange nvtx_range("pa_cache_write_scaled");
+    if (num_tokens < 0) return PA_ERR_INVALID_ARG;
+    ScaledWrite w{};
+    const pa_status st = check_scaled(key_cache, value_cache, key_scales, value_scales, cache, w.pool);
+    if (st != PA_OK || num_tokens == 0) return st;
+    if (!key || !value || !slot_mapping || !aligned16(key) || !aligned16(value)) return PA_ERR_INVALID_ARG;
+    const int64_t row = (int64_t)cache->num_kv_heads * cache->head_dim;
+    // rows are read 16 bytes at a time
+    if (key_stride < row || value_stride < row || key_stride % 8 != 0 || value_stride % 8 != 0)
+        return PA_ERR_INVALID_ARG;
+    w.key = key;
+    w.value = value;
+    w.key_stride = key_stride;
+    w.value_stride = value_stride;
+    w.slots = slot_mapping;
+    w.num_tokens = num_tokens;
+    w.err = err_flag;
+    const cudaError_t e = launch_cache_write_scaled(w, static_cast<cudaStream_t>(stream));
+    return e == cudaErrorNotSupported ? PA_ERR_UNSUPPORTED : from_cuda(e);
+}
+
+pa_status pa_copy_blocks_scaled(void *key_cache, void *value_cache, float *key_scales, float *value_scales,
+                                const int32_t *src_dst_pairs, int32_t num_pairs, const pa_cache_desc *cache,
+                                int32_t *err_flag, void *stream) {
+    const NvtxRange nvtx_range("pa_copy_blocks_scaled");
+    if (num_pairs < 0) return PA_ERR_INVALID_ARG;
+    ScaledPool pool;
+    const pa_status st = check_scaled(key_cache, value_cache, key_scales, value_scales, cache, pool);
+    if (st != PA_OK || num_pairs == 0) return st;
+    if (!src_dst_pairs) return PA_ERR_INVALID_ARG;
+    return from_cuda(launch_copy_blocks_scaled(pool, src_dst_pairs, num_pairs, err_flag,
+                                               static_cast<cudaStream_t>(stream)));
+}
+
+size_t pa_decode_scaled_workspace_size(int32_t num_q_heads, int32_t num_kv_heads, int32_t head_dim) {
+    if (num_q_heads <= 0 || num_kv_heads <= 0 || head_dim <= 0 || num_q_heads % num_kv_heads != 0) return 0;
+    return scaled_decode_workspace(num_q_heads, num_kv_heads, head_dim);
+}
+
+pa_status pa_decode_scaled(const void *query, const void *key_cache, const void *value_cache,
+                           const float *key_scales, const float *value_scales, const int32_t *block_tables,
+                           int32_t max_blocks_per_seq, const int32_t *context_lens, int32_t max_context_len,
+                           int32_t num_seqs, int32_t num_q_heads, float scale, void *workspace,
+                           size_t workspace_bytes, void *out, const pa_cache_desc *cache, int32_t *err_flag,
+                           void *stream) {
+    const NvtxRange nvtx_range("pa_decode_scaled");
+    ScaledDecode a{};
+    pa_status st = check_scaled(key_cache, value_cache, key_scales, value_scales, cache, a.pool);
+    if (st != PA_OK) return st;
+    st = check_group(num_q_heads, cache->num_kv_heads);
+    if (st != PA_OK) return st;
+    if (num_seqs < 0 || max_blocks_per_seq < 0 || max_context_len < 0) return PA_ERR_INVALID_ARG;
+    if (num_seqs == 0) return PA_OK;
+    if (num_seqs > 16384) return PA_ERR_UNSUPPORTED;
+    if (!query || !block_tables || !context_lens || !out || !workspace) return PA_ERR_INVALID_ARG;
+    if (!aligned16(query) || !aligned16(out) || !aligned16(workspace)) return PA_ERR_INVALID_ARG;
+    if (workspace_bytes < pa_decode_scaled_workspace_size(num_q_heads, cache->num_kv_heads, cache->head_dim))
+        return PA_ERR_INVALID_ARG;
+    if ((int64_t)max_context_len > (int64_t)max_blocks_per_seq * kBlockSize) return PA_ERR_INVALID_ARG;
+    // items (blocks and one more per sequence) are counted in 32 bits
+    if ((int64_t)num_seqs * ((int64_t)max_context_len / kBlockSize + 2) > INT32_MAX) return PA_ERR_UNSUPPORTED;
+    a.query = query;
+    a.tables = block_tables;
+    a.max_blocks = max_blocks_per_seq;
+    a.lens = context_lens;
+    a.max_context = max_context_len;
+    a.num_seqs = num_seqs;
+    a.num_q_heads = num_q_heads;
+    a.scale = scale;
+    a.workspace = workspace;
+    a.out = out;
+    a.err = err_flag;
+    return from_cuda(launch_decode_scaled(a, static_cast<cudaStream_t>(stream)));
 }
 
 pa_status pa_wait(void *stream, const int32_t *err_flag, int32_t timeout_ms, int32_t *flag_out) {
