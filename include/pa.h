@@ -423,6 +423,38 @@ PA_API pa_status pa_decode_scaled(const void *query, const void *key_cache, cons
                                   int32_t num_q_heads, float scale, void *workspace, size_t workspace_bytes,
                                   void *out, const pa_cache_desc *cache, int32_t *err_flag, void *stream);
 
+/* Bytes of workspace pa_prefill_packed needs (its job list). */
+PA_API size_t pa_prefill_packed_workspace_size(int32_t num_tokens, int32_t num_seqs, int32_t num_q_heads,
+                                               int32_t num_kv_heads);
+
+/*
+ * Causal attention over whole prompts packed without padding, before (or without) any
+ * cache: sequence s owns rows seq_starts[s] .. seq_starts[s + 1] - 1 (int32
+ * [num_seqs + 1], ascending, as pa_step_plan writes it) of query, key, value and out, and
+ *   out[i][h] = sum_{j <= i, j in s} softmax_j(scale * <query[i][h], key[j][h / g]>) value[j][h / g].
+ * query, out: bf16 [num_tokens, num_q_heads, head_dim]; key, value: bf16 [num_tokens,
+ * num_kv_heads, head_dim]; a token's heads and dims are contiguous, the tokens of query,
+ * key and value *_stride elements apart (at least a token's size, a multiple of 8: views of
+ * one fused projection are taken as they are); out is contiguous and must not overlap the
+ * inputs.  head_dim 64 or 128, num_q_heads / num_kv_heads in {1, 2, 4, 8}.  Rows outside
+ * every sequence are neither read as keys nor written.  Values and scores of keys
+ * behind a row never reach it, infinities and NaN included.
+ * A sequence whose starts do not ascend, leave [0, num_tokens] or span more than
+ * max_seq_len tokens sets PA_DEVERR_CHUNK and is skipped.  num_seqs <= 16384.
+ * tcgen05 tensor-core tiles, bf16 operands, fp32 accumulation, softmax statistics and
+ * sums; probabilities are rounded to bf16 for the product with V.  Two kernels (the
+ * first lists the jobs from the lengths, in `workspace`, whose contents need not be set;
+ * calls that overlap on the GPU need workspaces of their own).  Replays correctly from a
+ * graph, following seq_starts.
+ * Source: chenxutan 2.3 (prefill computes the whole prompt, compute bound).
+ */
+PA_API pa_status pa_prefill_packed(const void *query, const void *key, const void *value, int64_t query_stride,
+                                   int64_t key_stride, int64_t value_stride, const int32_t *seq_starts,
+                                   int32_t num_seqs, int32_t num_tokens, int32_t max_seq_len,
+                                   int32_t num_q_heads, int32_t num_kv_heads, int32_t head_dim, float scale,
+                                   void *workspace, size_t workspace_bytes, void *out, int32_t *err_flag,
+                                   void *stream);
+
 /*
  * Wait for `stream` to finish (polling, at most timeout_ms milliseconds) and read
  * the device error flag.  *flag_out (if not NULL) receives the flag value.

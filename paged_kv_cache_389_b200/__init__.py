@@ -64,6 +64,9 @@ def _load():
         "pa_copy_blocks_scaled": (C.c_int, [vp, vp, vp, vp, vp, i32, desc, vp, vp]),
         "pa_decode_scaled_workspace_size": (sz, [i32, i32, i32]),
         "pa_decode_scaled": (C.c_int, [vp, vp, vp, vp, vp, vp, i32, vp, i32, i32, i32, f32, vp, sz, vp, desc, vp, vp]),
+        "pa_prefill_packed_workspace_size": (sz, [i32, i32, i32, i32]),
+        "pa_prefill_packed": (C.c_int, [vp, vp, vp, i64, i64, i64, vp, i32, i32, i32, i32, i32, i32, f32, vp, sz, vp,
+                                        vp, vp]),
         "pa_wait": (C.c_int, [vp, vp, i32, C.POINTER(i32)]),
         "pa_set_wait_timeout_ns": (C.c_uint64, [C.c_uint64]),
         "pa_bm_create": (C.c_int, [i32, i32, vp, C.POINTER(vp)]),
@@ -105,7 +108,7 @@ EXPORTED = (
     "pa_abi_version", "pa_status_string", "pa_cache_write", "pa_copy_blocks", "pa_check_copy_pairs",
     "pa_decode_workspace_size", "pa_decode_launches", "pa_decode", "pa_append_decode", "pa_prefill_chunk",
     "pa_step_plan", "pa_step_release", "pa_cache_write_scaled", "pa_copy_blocks_scaled",
-    "pa_decode_scaled_workspace_size", "pa_decode_scaled",
+    "pa_decode_scaled_workspace_size", "pa_decode_scaled", "pa_prefill_packed_workspace_size", "pa_prefill_packed",
     "pa_wait", "pa_set_wait_timeout_ns",
 )
 
@@ -438,6 +441,30 @@ def pa_decode_scaled(query, key_cache, value_cache, key_scales, value_scales, bl
          key_scales.data_ptr(), value_scales.data_ptr(), block_tables.data_ptr(), block_tables.shape[1],
          context_lens.data_ptr(), int(max_context_len), S, hq, float(scale), workspace.data_ptr(),
          workspace.numel() * workspace.element_size(), out.data_ptr(), d, _addr(err_flag))
+
+
+def pa_prefill_packed_workspace_size(num_tokens, num_seqs, num_q_heads, num_kv_heads) -> int:
+    return int(_lib.pa_prefill_packed_workspace_size(num_tokens, num_seqs, num_q_heads, num_kv_heads))
+
+
+def pa_prefill_packed(query, key, value, seq_starts, max_seq_len, scale, out, workspace, err_flag=None, stream=None):
+    """Causal attention over packed prompts; query/out bf16 [T, Hq, d], key/value [T, Hkv, d]
+    (their tokens may be strided), seq_starts int32 [S + 1], workspace of
+    pa_prefill_packed_workspace_size(T, S, Hq, Hkv) bytes."""
+    torch = _torch()
+    T, hq, hd = query.shape
+    hkv, S = key.shape[1], seq_starts.shape[0] - 1
+    bf16 = torch.bfloat16
+    assert query.dtype == bf16 == key.dtype and value.dtype == bf16 == out.dtype
+    assert key.shape[0] == T == value.shape[0] and out.shape == query.shape and out.is_contiguous()
+    assert S >= 0 and workspace.is_contiguous()
+    qs, ks, vs = (_token_rows(query, hq, hd, "query"), _token_rows(key, hkv, hd, "key"),
+                  _token_rows(value, hkv, hd, "value"))
+    _check_int(seq_starts, torch.int32, (S + 1,), "seq_starts")
+    dev = _on_device(query, key, value, seq_starts, out, workspace, err_flag)
+    _run("pa_prefill_packed", dev, stream, query.data_ptr(), key.data_ptr(), value.data_ptr(), qs, ks, vs,
+         seq_starts.data_ptr(), S, T, int(max_seq_len), hq, hkv, hd, float(scale), workspace.data_ptr(),
+         workspace.numel() * workspace.element_size(), out.data_ptr(), _addr(err_flag))
 
 
 def pa_wait(err_flag=None, stream=None, timeout_ms: int = 10000) -> int:

@@ -446,6 +446,41 @@ pa_status pa_decode_scaled(const void *query, const void *key_cache, const void 
     return from_cuda(launch_decode_scaled(a, static_cast<cudaStream_t>(stream)));
 }
 
+size_t pa_prefill_packed_workspace_size(int32_t num_tokens, int32_t num_seqs, int32_t num_q_heads,
+                                        int32_t num_kv_heads) {
+    if (num_tokens < 0 || num_seqs < 0 || num_q_heads <= 0 || num_kv_heads <= 0 || num_q_heads % num_kv_heads != 0)
+        return 0;
+    return packed_workspace(num_tokens, num_seqs, num_q_heads / num_kv_heads);
+}
+
+pa_status pa_prefill_packed(const void *query, const void *key, const void *value, int64_t query_stride,
+                            int64_t key_stride, int64_t value_stride, const int32_t *seq_starts, int32_t num_seqs,
+                            int32_t num_tokens, int32_t max_seq_len, int32_t num_q_heads, int32_t num_kv_heads,
+                            int32_t head_dim, float scale, void *workspace, size_t workspace_bytes, void *out,
+                            int32_t *err_flag, void *stream) {
+    const NvtxRange nvtx_range("pa_prefill_packed");
+    if (num_kv_heads <= 0) return PA_ERR_INVALID_ARG;
+    const pa_status st = check_group(num_q_heads, num_kv_heads);
+    if (st != PA_OK) return st;
+    if (head_dim != 64 && head_dim != 128) return PA_ERR_UNSUPPORTED;
+    if (num_seqs < 0 || num_tokens < 0 || max_seq_len < 0) return PA_ERR_INVALID_ARG;
+    if (num_seqs == 0 || num_tokens == 0 || max_seq_len == 0) return PA_OK;
+    if (num_seqs > kMaxPlanSeqs) return PA_ERR_UNSUPPORTED;
+    if (!query || !key || !value || !seq_starts || !out || !workspace) return PA_ERR_INVALID_ARG;
+    if (!aligned16(query) || !aligned16(key) || !aligned16(value) || !aligned16(out) || !aligned16(workspace))
+        return PA_ERR_INVALID_ARG;
+    // tiles are fetched 16 bytes at a time
+    const int64_t q_row = (int64_t)num_q_heads * head_dim, kv_row = (int64_t)num_kv_heads * head_dim;
+    if (query_stride < q_row || key_stride < kv_row || value_stride < kv_row) return PA_ERR_INVALID_ARG;
+    if (query_stride % 8 != 0 || key_stride % 8 != 0 || value_stride % 8 != 0) return PA_ERR_INVALID_ARG;
+    if (workspace_bytes < pa_prefill_packed_workspace_size(num_tokens, num_seqs, num_q_heads, num_kv_heads))
+        return PA_ERR_INVALID_ARG;
+    const PackedPrefill a{query, key, value, query_stride, key_stride, value_stride, seq_starts, num_tokens, num_seqs,
+                          max_seq_len, num_q_heads, num_kv_heads, head_dim, scale, workspace, out, err_flag};
+    const cudaError_t e = launch_prefill_packed(a, static_cast<cudaStream_t>(stream));
+    return e == cudaErrorNotSupported ? PA_ERR_UNSUPPORTED : from_cuda(e);
+}
+
 pa_status pa_wait(void *stream, const int32_t *err_flag, int32_t timeout_ms, int32_t *flag_out) {
     const NvtxRange nvtx_range("pa_wait");
     cudaStream_t s = static_cast<cudaStream_t>(stream);

@@ -71,4 +71,19 @@ struct ScaledDecode {
 size_t scaled_decode_workspace(int32_t num_q_heads, int32_t num_kv_heads, int32_t head_dim);
 cudaError_t launch_decode_scaled(const ScaledDecode &a, cudaStream_t stream);
 
+// ---- attention over packed prompts ---------------------------------------------------
+struct PackedPrefill {
+    const void *query, *key, *value;              // bf16 [T][heads][head_dim], tokens strided (elements)
+    int64_t q_stride, k_stride, v_stride;
+    const int32_t *starts;
+    int32_t num_tokens, num_seqs, max_seq_len, num_q_heads, num_kv_heads, head_dim;
+    float scale;
+    void *workspace;
+    void *out;                                    // [T][Hq][head_dim]
+    int32_t *err;
+};
+
+size_t packed_workspace(int32_t num_tokens, int32_t num_seqs, int32_t g);
+cudaError_t launch_prefill_packed(const PackedPrefill &a, cudaStream_t stream);
+
 }  // namespace pa
