@@ -77,8 +77,8 @@ def check(got, q, k, v, starts, scale):
         rows[a:b] = True
     g = f(got)
     assert (g[~rows] == 7).all()              # rows of no sequence are left alone
-    # P is rounded to bf16 (2^-8); a quarter of the exponentials are off by up to 2^-13
-    bound = step_ops.attention_bound(ref, mass, reach, (0, 2.0 ** -8 + 2 * 2.0 ** -13, 0.0))
+    # P is rounded to bf16 (2^-8)
+    bound = step_ops.attention_bound(ref, mass, reach, (0, 2.0 ** -8, 0.0))
     far = (np.abs(g - ref) - bound)[rows]
     assert np.isfinite(g[rows]).all() and (far <= 0).all(), f"off by {far.max():.3g} more than the bound"
 
@@ -149,7 +149,7 @@ def test_what_is_masked_never_reaches_a_row(pa, hq, hkv, d):
             seq = (starts[:-1][starts[:-1] <= at.start].max(), min([s for s in starts if s > at.start], default=500))
             same = [i for i in range(470) if i < at.start or i >= seq[1]]
             ref, mass, reach = step_ops.packed_attention(*(x.double().cpu().numpy() for x in (q, k, v)), starts, 0.1)
-            bound = step_ops.attention_bound(ref, mass, reach, (0, 2.0 ** -8 + 2 * 2.0 ** -13, 0.0))
+            bound = step_ops.attention_bound(ref, mass, reach, (0, 2.0 ** -8, 0.0))
             g = out.double().cpu().numpy()
             assert (np.abs(g - ref) <= bound)[same].all()
             if at.start < 470 and bad_v != bad_v:
@@ -169,6 +169,11 @@ def test_bad_starts_are_flagged(pa):
         a, b = good[0]
         only = out.clone()
         only[:a], only[b:] = 7, 7
+        if starts == (0, 100, 90, 300):
+            # rows 90 .. 99 are also the first ones of the (valid) third sequence: both write them
+            only = only[:90]
+            check(only, q[:90], k[:90], v[:90], np.array([0, 90]), 0.1)
+            continue
         check(only, q, k, v, np.array([a, b]), 0.1)
     out, flag = run(pa, q, k, v, (0, 100, 300), 0.1)
     assert flag == 0
