@@ -22,8 +22,13 @@
 // What bounds it.  d = 128: per 80-key tile of both streams the tensor core needs 1,490
 // clocks (measured alone; S with both operands in shared memory reads them at the
 // bank limit), the special-function units 1,280 for the exponentials; a step takes about
-// 1,850, and the clock is down to 1.56 GHz at the power limit.  2 x 8192 tokens, 64/8 heads: 1.79 ms, 1,227 TFLOP/s.
+// 1,850, and the clock is down to 1.56 GHz at the power limit.  2 x 8192 tokens, 64/8 heads: 1.75 ms,
+// 1,250 TFLOP/s; 16 x 1024 tokens, 32/8 heads: 0.17 ms, 815 TFLOP/s, where a job has 7 tiles and its
+// output rows (4,000 clocks) are no longer small beside them.
 // d = 64: the products are half as long, the exponentials are not: 2,048 clocks of a step's 2,900.
+// Tried and slower: output rows written by four more warps (128 registers a thread at launch:
+// 184 us against 170 for 16 x 1024 tokens) or after the next job's first tile (189); jobs
+// ordered by sequence instead of longest first (177).
 // A share of the exponentials on the FMA units (a cubic in the fraction) was tried at 1, 2
 // and 3 of 8: no gain at d = 128, 3 to 9 % slower at d = 64, so there is none.
 //
@@ -467,10 +472,12 @@ __global__ void __launch_bounds__(kThreads, 1) packed_prefill_kernel(const __gri
                     if (tail) {
                         ++nland;
                         // whole rows become zero: the swizzle moves chunks within a row only
-                        for (int x = lane; x < (kKeys - seen) * 8 * SM::kHalves; x += 32) {
-                            const int f = x / ((kKeys - seen) * 8), r = x % ((kKeys - seen) * 8);
-                            *reinterpret_cast<uint4 *>(smem + SM::kV + st * kTileBytes + f * kHalf + seen * 128 + r * 16) =
-                                make_uint4(0, 0, 0, 0);
+                        const int bytes = (kKeys - seen) * 128;
+#pragma unroll
+                        for (int f = 0; f < SM::kHalves; ++f) {
+                            unsigned char *rows = smem + SM::kV + st * kTileBytes + f * kHalf + seen * 128;
+                            for (int x = lane * 16; x < bytes; x += 512)
+                                *reinterpret_cast<uint4 *>(rows + x) = make_uint4(0, 0, 0, 0);
                         }
                         fence_proxy_async_smem();
                         __syncwarp();
@@ -661,43 +668,53 @@ __global__ void __launch_bounds__(kThreads, 1) packed_prefill_kernel(const __gri
             ++nuse;
             tc::fence_after();
             const float inv = l > 0.f ? 1.f / l : l;      // NaN stays NaN
-            bool odd = false;
             // Through shared memory, so that a store covers whole 128-byte lines (a row per
-            // thread and store touches 32 lines: 7,400 clocks per job instead of 1,900).
+            // thread and store would touch 32 of them).
             unsigned char *stage = smem + SM::kOut + warp * kOutBytes;
+            const uint32_t head_bytes = D * 2, tok_bytes = (uint32_t)p.num_q_heads * head_bytes;
+            unsigned char *out0 = p.out + (int64_t)(jb.row0 + jb.i0 + t * kTok) * tok_bytes + jb.h * G * head_bytes +
+                                  (lane & 7) * 16;
+            const float2 inv2 = make_float2(inv, inv), zero2 = make_float2(0.f, 0.f);
+            float2 bad0 = zero2, bad1 = zero2;           // NaN once anything is not finite
 #pragma unroll
             for (int c = 0; c < D; c += 64) {
                 float o[64];
 #pragma unroll
                 for (int x = 0; x < 64; x += 16) tc::ld16(tO + c + x, o + x);
                 tc::wait_ld();
-                float bad = 0.f;
 #pragma unroll
                 for (int x = 0; x < 8; ++x) {
                     uint32_t w[4];
 #pragma unroll
                     for (int y = 0; y < 4; ++y) {
-                        const float a = o[8 * x + 2 * y] * inv, b = o[8 * x + 2 * y + 1] * inv;
-                        bad = fmaf(a, 0.f, fmaf(b, 0.f, bad));   // NaN once anything is not finite
-                        w[y] = pack_bf16x2(a, b);
+                        const float2 v = __fmul2_rn(make_float2(o[8 * x + 2 * y], o[8 * x + 2 * y + 1]), inv2);
+                        if (y & 1) bad1 = __ffma2_rn(v, zero2, bad1);
+                        else bad0 = __ffma2_rn(v, zero2, bad0);
+                        w[y] = pack_bf16x2(v.x, v.y);
                     }
                     *reinterpret_cast<uint4 *>(stage + lane * 128 + ((x ^ (lane & 7)) << 4)) = make_uint4(w[0], w[1], w[2], w[3]);
                 }
-                odd |= bad != 0.f;
+                if (c + 64 >= D) {       // O_t has been read
+                    tc::fence_before();
+                    mbar_arrive(&bars[kBarOFree + t]);
+                }
                 __syncwarp();
+                uint4 w[8];
 #pragma unroll
                 for (int x = 0; x < 8; ++x) {
-                    const int rl = 4 * x + (lane >> 3), ch = lane & 7;   // row of the warp, 16-byte chunk
-                    const int rr = qd * 32 + rl;
-                    const uint4 w = *reinterpret_cast<const uint4 *>(stage + rl * 128 + ((ch ^ (rl & 7)) << 4));
-                    const int64_t row = (int64_t)(jb.row0 + jb.i0 + t * kTok + rr / G) * p.num_q_heads + jb.h * G + rr % G;
-                    if (rr < jb.nrows[t]) *reinterpret_cast<uint4 *>(p.out + row * (D * 2) + c * 2 + ch * 16) = w;
+                    const int rl = 4 * x + (lane >> 3);                      // row of the warp
+                    w[x] = *reinterpret_cast<const uint4 *>(stage + rl * 128 + (((lane & 7) ^ (rl & 7)) << 4));
+                }
+#pragma unroll
+                for (int x = 0; x < 8; ++x) {
+                    const int rr = qd * 32 + 4 * x + (lane >> 3);            // row of the tile
+                    if (rr < jb.nrows[t])
+                        *reinterpret_cast<uint4 *>(out0 + ((uint32_t)(rr / G) * tok_bytes + (rr % G) * head_bytes) + c * 2) = w[x];
                 }
                 __syncwarp();
             }
-            tc::fence_before();
-            mbar_arrive(&bars[kBarOFree + t]);
-            unsigned again = __ballot_sync(kFull, odd && row_ok);
+            const bool odd = (bad0.x + bad0.y) + (bad1.x + bad1.y) != 0.f;
+            unsigned again = __ballot_sync(kFull, odd && r < jb.nrows[t]);
             while (again) {
                 const int ln = __ffs(again) - 1;
                 again &= again - 1;
