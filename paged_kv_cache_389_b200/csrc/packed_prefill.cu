@@ -831,9 +831,10 @@ cudaError_t launch_prefill_packed(const PackedPrefill &a, cudaStream_t stream) {
     cudaError_t e = cudaGetDevice(&dev);
     if (e != cudaSuccess) return e;
     const size_t plan_smem = (size_t)(a.num_seqs + 1) * 4;
-    if ((e = cudaFuncSetAttribute(packed_plan_kernel, cudaFuncAttributeMaxDynamicSharedMemorySize,
-                                  (kMaxPlanSeqs + 1) * 4)) != cudaSuccess)
-        return e;
+    if (plan_smem > 46 * 1024) {   // with its static arrays above what a launch may ask for anyway
+        e = cudaFuncSetAttribute(packed_plan_kernel, cudaFuncAttributeMaxDynamicSharedMemorySize, (kMaxPlanSeqs + 1) * 4);
+        if (e != cudaSuccess) return e;
+    }
     packed_plan_kernel<<<1, kPlanThreads, plan_smem, stream>>>(pl);
     if ((e = cudaGetLastError()) != cudaSuccess) return e;
     const int grid = (int)std::min<int64_t>(jobs * a.num_kv_heads, num_sms(dev));

@@ -201,10 +201,12 @@ __global__ void __launch_bounds__(kPlanThreads, 1) step_plan_kernel(const StepPl
 template <bool kRelease, bool kCluster>
 cudaError_t launch(const StepPlan &p, int ctas, cudaStream_t stream) {
     const size_t smem = (size_t)(3 * (p.num_seqs + 1)) * 4;
-    cudaError_t e = cudaFuncSetAttribute(step_plan_kernel<kRelease, kCluster>,
-                                         cudaFuncAttributeMaxDynamicSharedMemorySize,
-                                         3 * (kMaxPlanSeqs + 1) * 4);
-    if (e != cudaSuccess) return e;
+    if (smem > 48 * 1024) {   // above what a launch may ask for anyway
+        const cudaError_t e = cudaFuncSetAttribute(step_plan_kernel<kRelease, kCluster>,
+                                                   cudaFuncAttributeMaxDynamicSharedMemorySize,
+                                                   3 * (kMaxPlanSeqs + 1) * 4);
+        if (e != cudaSuccess) return e;
+    }
     cudaLaunchConfig_t cfg = {};
     cfg.gridDim = dim3((unsigned)ctas);
     cfg.blockDim = dim3(kPlanThreads);
