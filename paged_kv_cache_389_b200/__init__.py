@@ -280,36 +280,30 @@ def pa_prefill_chunk(query, key_cache, value_cache, block_tables, context_lens, 
 # or on that device's current stream.  The smallest of them take a few microseconds on the
 # GPU, so the checks are written for their cost (current_stream() alone takes 2 to 3 us; the
 # raw handle 0.1).
-def _run(name, dev, stream, *args):
-    """Call the library with the stream's handle appended, with device `dev` current."""
-    torch = _torch()
-    fn = getattr(_lib, name)
-    handle = torch._C._cuda_getCurrentRawStream(dev) if stream is None else stream.cuda_stream
-    if dev == torch.cuda.current_device():
+def _run(fn, name, dev, stream, *args):
+    """Call the library's fn with the stream's handle appended, with device `dev` current."""
+    assert dev >= 0, "tensors passed to the library must be on a CUDA device"
+    cuda = _torch().cuda
+    handle = _torch()._C._cuda_getCurrentRawStream(dev) if stream is None else stream.cuda_stream
+    if dev == cuda.current_device():
         status = fn(*args, handle)
     else:
-        with torch.cuda.device(dev):
+        with cuda.device(dev):
             status = fn(*args, handle)
     if status != PA_OK:
         raise PAError(status, name)
 
 
-def _on_device(*tensors):
-    """Index of the CUDA device all tensors (None skipped) are on."""
-    dev = tensors[0].get_device()
-    assert dev >= 0, "tensors passed to the library must be on a CUDA device"
-    for t in tensors:
-        assert t is None or t.get_device() == dev, "tensors of one call must be on one CUDA device"
-    return dev
+def _p(t, dtype, shape, dev, what):
+    """Address of a contiguous tensor of this type and shape on device `dev`."""
+    if t.dtype != dtype or t.shape != shape or t.get_device() != dev or not t.is_contiguous():
+        raise AssertionError(f"{what}: contiguous {dtype} of shape {tuple(shape)} on device {dev} wanted, got {t.dtype} "
+                             f"{tuple(t.shape)} on {t.device}")
+    return t.data_ptr()
 
 
-def _check_int(t, dtype, shape, what):
-    assert t.dtype == dtype and t.shape == shape and t.is_contiguous(), \
-        f"{what}: contiguous {dtype} of shape {tuple(shape)} wanted, got {t.dtype} {tuple(t.shape)}"
-
-
-def _addr(t):
-    return None if t is None else t.data_ptr()
+def _flag(err_flag, dev):
+    return None if err_flag is None else _p(err_flag, _torch().int32, (1,), dev, "err_flag")
 
 
 def pa_step_plan(counts, context_lens, block_tables, free_blocks, num_free, slot_mapping, seq_starts,
@@ -318,131 +312,115 @@ def pa_step_plan(counts, context_lens, block_tables, free_blocks, num_free, slot
     sequence.  counts, context_lens int32 [S]; block_tables int32 [S, max_blocks] (extended in
     place); free_blocks int32 [N] with its height num_free int32 [1]; out: slot_mapping int64
     [capacity], seq_starts int32 [S + 1], new_context_lens and new_num_free (default: in place)."""
-    torch = _torch()
-    i32 = torch.int32
-    new_context_lens = context_lens if new_context_lens is None else new_context_lens
-    new_num_free = num_free if new_num_free is None else new_num_free
-    S = counts.shape[0]
-    _check_int(counts, i32, (S,), "counts")
-    _check_int(context_lens, i32, (S,), "context_lens")
-    _check_int(new_context_lens, i32, (S,), "new_context_lens")
-    _check_int(seq_starts, i32, (S + 1,), "seq_starts")
-    _check_int(num_free, i32, (1,), "num_free")
-    _check_int(new_num_free, i32, (1,), "new_num_free")
-    assert block_tables.dim() == 2 and free_blocks.dim() == 1 and slot_mapping.dim() == 1
-    _check_int(block_tables, i32, (S, block_tables.shape[1]), "block_tables")
-    _check_int(free_blocks, i32, free_blocks.shape, "free_blocks")
-    _check_int(slot_mapping, torch.int64, slot_mapping.shape, "slot_mapping")
-    dev = _on_device(counts, context_lens, block_tables, free_blocks, num_free, slot_mapping, seq_starts,
-                     new_context_lens, new_num_free, err_flag)
-    _run("pa_step_plan", dev, stream, counts.data_ptr(), context_lens.data_ptr(), S, block_tables.data_ptr(),
-         block_tables.shape[1], free_blocks.data_ptr(), free_blocks.shape[0], num_free.data_ptr(),
-         slot_mapping.data_ptr(), slot_mapping.shape[0], seq_starts.data_ptr(), new_context_lens.data_ptr(),
-         new_num_free.data_ptr(), _addr(err_flag))
+    i32, dev = _torch().int32, counts.get_device()
+    S, = counts.shape
+    mb = block_tables.shape[-1]
+    N, = free_blocks.shape
+    cap, = slot_mapping.shape
+    lens = _p(context_lens, i32, (S,), dev, "context_lens")
+    height = _p(num_free, i32, (1,), dev, "num_free")
+    _run(_lib.pa_step_plan, "pa_step_plan", dev, stream, _p(counts, i32, (S,), dev, "counts"), lens, S,
+         _p(block_tables, i32, (S, mb), dev, "block_tables"), mb, _p(free_blocks, i32, (N,), dev, "free_blocks"), N, height,
+         _p(slot_mapping, _torch().int64, (cap,), dev, "slot_mapping"), cap, _p(seq_starts, i32, (S + 1,), dev, "seq_starts"),
+         lens if new_context_lens is None else _p(new_context_lens, i32, (S,), dev, "new_context_lens"),
+         height if new_num_free is None else _p(new_num_free, i32, (1,), dev, "new_num_free"), _flag(err_flag, dev))
 
 
 def pa_step_release(finished, context_lens, block_tables, free_blocks, num_free, new_context_lens=None,
                     new_num_free=None, err_flag=None, stream=None):
     """Give the blocks of the sequences with finished[s] != 0 (int32 [S]) back to the stack."""
-    torch = _torch()
-    i32 = torch.int32
-    new_context_lens = context_lens if new_context_lens is None else new_context_lens
-    new_num_free = num_free if new_num_free is None else new_num_free
-    S = finished.shape[0]
-    for t, what in ((finished, "finished"), (context_lens, "context_lens"), (new_context_lens, "new_context_lens")):
-        _check_int(t, i32, (S,), what)
-    _check_int(num_free, i32, (1,), "num_free")
-    _check_int(new_num_free, i32, (1,), "new_num_free")
-    assert block_tables.dim() == 2 and free_blocks.dim() == 1
-    _check_int(block_tables, i32, (S, block_tables.shape[1]), "block_tables")
-    _check_int(free_blocks, i32, free_blocks.shape, "free_blocks")
-    dev = _on_device(finished, context_lens, block_tables, free_blocks, num_free, new_context_lens, new_num_free,
-                     err_flag)
-    _run("pa_step_release", dev, stream, finished.data_ptr(), context_lens.data_ptr(), S, block_tables.data_ptr(),
-         block_tables.shape[1], free_blocks.data_ptr(), free_blocks.shape[0], num_free.data_ptr(),
-         new_context_lens.data_ptr(), new_num_free.data_ptr(), _addr(err_flag))
+    i32, dev = _torch().int32, finished.get_device()
+    S, = finished.shape
+    mb = block_tables.shape[-1]
+    N, = free_blocks.shape
+    lens = _p(context_lens, i32, (S,), dev, "context_lens")
+    height = _p(num_free, i32, (1,), dev, "num_free")
+    _run(_lib.pa_step_release, "pa_step_release", dev, stream, _p(finished, i32, (S,), dev, "finished"), lens, S,
+         _p(block_tables, i32, (S, mb), dev, "block_tables"), mb, _p(free_blocks, i32, (N,), dev, "free_blocks"), N, height,
+         lens if new_context_lens is None else _p(new_context_lens, i32, (S,), dev, "new_context_lens"),
+         height if new_num_free is None else _p(new_num_free, i32, (1,), dev, "new_num_free"), _flag(err_flag, dev))
 
 
 @functools.lru_cache(maxsize=64)
-def _scaled_desc(shape, code):
-    return CacheDesc(*shape, code, 1.0, 1.0)
+def _scaled_desc(num_blocks, num_kv_heads, block_size, head_dim, code):
+    return CacheDesc(num_blocks, num_kv_heads, block_size, head_dim, code, 1.0, 1.0)
 
 
-def _scaled_pool(key_cache, value_cache, key_scales, value_scales):
-    """Descriptor of pools of torch.float8_e4m3fn or torch.int8 codes with float32 scales
-    [num_blocks, num_kv_heads]."""
+def _scaled_pool(key_cache, value_cache, key_scales, value_scales, dev):
+    """(key codes, value codes, key scales, value scales, descriptor) of pools of
+    torch.float8_e4m3fn or torch.int8 codes with float32 scales [num_blocks, num_kv_heads]."""
     torch = _torch()
-    dt = key_cache.dtype
+    dt, shape = key_cache.dtype, key_cache.shape
     if dt == torch.float8_e4m3fn:
         code = PA_FP8_E4M3
     elif dt == torch.int8:
         code = PA_INT8
     else:
         raise TypeError(f"unsupported dtype {dt}")
-    shape = key_cache.shape
-    assert value_cache.dtype == dt and value_cache.shape == shape and len(shape) == 4
-    assert key_cache.is_contiguous() and value_cache.is_contiguous()
-    _check_int(key_scales, torch.float32, shape[:2], "key_scales")
-    _check_int(value_scales, torch.float32, shape[:2], "value_scales")
-    return C.byref(_scaled_desc(tuple(shape), code))
+    nb, hkv, bs, d = shape
+    return (_p(key_cache, dt, shape, dev, "key_cache"), _p(value_cache, dt, shape, dev, "value_cache"),
+            _p(key_scales, torch.float32, (nb, hkv), dev, "key_scales"),
+            _p(value_scales, torch.float32, (nb, hkv), dev, "value_scales"), C.byref(_scaled_desc(nb, hkv, bs, d, code)))
 
 
-def _token_rows(t, heads, d, what):
-    """Elements between tokens of a [T, heads, d] tensor whose heads and dims are contiguous."""
-    assert t.dim() == 3 and t.shape[1] == heads and t.shape[2] == d, f"{what}: [T, {heads}, {d}] wanted"
-    assert t.stride(2) == 1 and (heads == 1 or t.stride(1) == d), f"{what}: heads and dims must be contiguous"
-    return t.stride(0) if t.shape[0] > 1 else heads * d
+def _rows(t, tokens, heads, d, dev, what):
+    """(address, elements between tokens) of bf16 [tokens, heads, d] whose heads and dims are
+    contiguous; the tokens may be further apart."""
+    st = t.stride()
+    if (t.dtype != _torch().bfloat16 or t.shape != (tokens, heads, d) or t.get_device() != dev or st[2] != 1
+            or (heads > 1 and st[1] != d)):
+        raise AssertionError(f"{what}: bf16 [{tokens}, {heads}, {d}] with contiguous heads and dims on device {dev} "
+                             f"wanted, got {t.dtype} {tuple(t.shape)} with strides {st} on {t.device}")
+    return t.data_ptr(), st[0] if tokens > 1 else heads * d
 
 
 def pa_cache_write_scaled(key, value, slot_mapping, key_cache, value_cache, key_scales, value_scales,
                           err_flag=None, stream=None):
     """Append key/value bf16 [T, Hkv, d] (tokens may be strided) at slot_mapping (int64 [T]) to
     8-bit pools with a power-of-two scale per (block, kv head)."""
-    torch = _torch()
-    d = _scaled_pool(key_cache, value_cache, key_scales, value_scales)
-    T, hkv, hd = key.shape[0], key_cache.shape[1], key_cache.shape[3]
-    assert key.dtype == torch.bfloat16 == value.dtype and value.shape[0] == T
-    ks, vs = _token_rows(key, hkv, hd, "key"), _token_rows(value, hkv, hd, "value")
-    _check_int(slot_mapping, torch.int64, (T,), "slot_mapping")
-    dev = _on_device(key, value, slot_mapping, key_cache, value_cache, key_scales, value_scales, err_flag)
-    _run("pa_cache_write_scaled", dev, stream, key.data_ptr(), value.data_ptr(), ks, vs, slot_mapping.data_ptr(), T,
-         key_cache.data_ptr(), value_cache.data_ptr(), key_scales.data_ptr(), value_scales.data_ptr(), d,
-         _addr(err_flag))
+    dev = key_cache.get_device()
+    kc, vc, ks, vs, desc = _scaled_pool(key_cache, value_cache, key_scales, value_scales, dev)
+    T = key.shape[0]
+    _, hkv, _, d = key_cache.shape
+    k, k_stride = _rows(key, T, hkv, d, dev, "key")
+    v, v_stride = _rows(value, T, hkv, d, dev, "value")
+    _run(_lib.pa_cache_write_scaled, "pa_cache_write_scaled", dev, stream, k, v, k_stride, v_stride,
+         _p(slot_mapping, _torch().int64, (T,), dev, "slot_mapping"), T, kc, vc, ks, vs, desc, _flag(err_flag, dev))
 
 
 def pa_copy_blocks_scaled(key_cache, value_cache, key_scales, value_scales, src_dst_pairs, err_flag=None, stream=None):
     """Copy whole blocks, codes and scales, src -> dst for each row of int32 [P, 2]."""
-    torch = _torch()
-    d = _scaled_pool(key_cache, value_cache, key_scales, value_scales)
-    assert src_dst_pairs.dim() == 2
-    _check_int(src_dst_pairs, torch.int32, (src_dst_pairs.shape[0], 2), "src_dst_pairs")
-    dev = _on_device(key_cache, value_cache, key_scales, value_scales, src_dst_pairs, err_flag)
-    _run("pa_copy_blocks_scaled", dev, stream, key_cache.data_ptr(), value_cache.data_ptr(), key_scales.data_ptr(),
-         value_scales.data_ptr(), src_dst_pairs.data_ptr(), src_dst_pairs.shape[0], d, _addr(err_flag))
+    dev = key_cache.get_device()
+    kc, vc, ks, vs, desc = _scaled_pool(key_cache, value_cache, key_scales, value_scales, dev)
+    P = src_dst_pairs.shape[0]
+    _run(_lib.pa_copy_blocks_scaled, "pa_copy_blocks_scaled", dev, stream, kc, vc, ks, vs,
+         _p(src_dst_pairs, _torch().int32, (P, 2), dev, "src_dst_pairs"), P, desc, _flag(err_flag, dev))
 
 
 def pa_decode_scaled_workspace_size(num_q_heads, num_kv_heads, head_dim) -> int:
     return int(_lib.pa_decode_scaled_workspace_size(num_q_heads, num_kv_heads, head_dim))
 
 
+def _workspace(t, dev):
+    assert t.get_device() == dev and t.is_contiguous(), "workspace: contiguous and on the other tensors' device"
+    return t.data_ptr(), t.numel() * t.element_size()
+
+
 def pa_decode_scaled(query, key_cache, value_cache, key_scales, value_scales, block_tables, context_lens,
                      max_context_len, scale, out, workspace, err_flag=None, stream=None):
     """Decode attention over 8-bit pools with a scale per (block, kv head); query/out bf16
     [S, Hq, d]; workspace of pa_decode_scaled_workspace_size(Hq, Hkv, d) bytes."""
-    torch = _torch()
-    d = _scaled_pool(key_cache, value_cache, key_scales, value_scales)
-    S, hq, hd = query.shape
-    assert query.dtype == torch.bfloat16 == out.dtype and out.shape == query.shape and hd == key_cache.shape[3]
-    assert query.is_contiguous() and out.is_contiguous() and workspace.is_contiguous()
-    assert block_tables.dim() == 2
-    _check_int(block_tables, torch.int32, (S, block_tables.shape[1]), "block_tables")
-    _check_int(context_lens, torch.int32, (S,), "context_lens")
-    dev = _on_device(query, key_cache, value_cache, key_scales, value_scales, block_tables, context_lens, out, workspace,
-                     err_flag)
-    _run("pa_decode_scaled", dev, stream, query.data_ptr(), key_cache.data_ptr(), value_cache.data_ptr(),
-         key_scales.data_ptr(), value_scales.data_ptr(), block_tables.data_ptr(), block_tables.shape[1],
-         context_lens.data_ptr(), int(max_context_len), S, hq, float(scale), workspace.data_ptr(),
-         workspace.numel() * workspace.element_size(), out.data_ptr(), d, _addr(err_flag))
+    torch, dev = _torch(), key_cache.get_device()
+    kc, vc, ks, vs, desc = _scaled_pool(key_cache, value_cache, key_scales, value_scales, dev)
+    shape = query.shape
+    S, hq, d = shape
+    assert d == key_cache.shape[3], "query: head_dim of the pools wanted"
+    mb = block_tables.shape[-1]
+    ws, ws_bytes = _workspace(workspace, dev)
+    _run(_lib.pa_decode_scaled, "pa_decode_scaled", dev, stream, _p(query, torch.bfloat16, shape, dev, "query"), kc, vc, ks, vs,
+         _p(block_tables, torch.int32, (S, mb), dev, "block_tables"), mb,
+         _p(context_lens, torch.int32, (S,), dev, "context_lens"), int(max_context_len), S, hq, float(scale), ws, ws_bytes,
+         _p(out, torch.bfloat16, shape, dev, "out"), desc, _flag(err_flag, dev))
 
 
 def pa_prefill_packed_workspace_size(num_tokens, num_seqs, num_q_heads, num_kv_heads) -> int:
@@ -453,20 +431,16 @@ def pa_prefill_packed(query, key, value, seq_starts, max_seq_len, scale, out, wo
     """Causal attention over packed prompts; query/out bf16 [T, Hq, d], key/value [T, Hkv, d]
     (their tokens may be strided), seq_starts int32 [S + 1], workspace of
     pa_prefill_packed_workspace_size(T, S, Hq, Hkv) bytes."""
-    torch = _torch()
-    T, hq, hd = query.shape
+    torch, dev = _torch(), query.get_device()
+    T, hq, d = query.shape
     hkv, S = key.shape[1], seq_starts.shape[0] - 1
-    bf16 = torch.bfloat16
-    assert query.dtype == bf16 == key.dtype and value.dtype == bf16 == out.dtype
-    assert key.shape[0] == T == value.shape[0] and out.shape == query.shape and out.is_contiguous()
-    assert S >= 0 and workspace.is_contiguous()
-    qs, ks, vs = (_token_rows(query, hq, hd, "query"), _token_rows(key, hkv, hd, "key"),
-                  _token_rows(value, hkv, hd, "value"))
-    _check_int(seq_starts, torch.int32, (S + 1,), "seq_starts")
-    dev = _on_device(query, key, value, seq_starts, out, workspace, err_flag)
-    _run("pa_prefill_packed", dev, stream, query.data_ptr(), key.data_ptr(), value.data_ptr(), qs, ks, vs,
-         seq_starts.data_ptr(), S, T, int(max_seq_len), hq, hkv, hd, float(scale), workspace.data_ptr(),
-         workspace.numel() * workspace.element_size(), out.data_ptr(), _addr(err_flag))
+    q, q_stride = _rows(query, T, hq, d, dev, "query")
+    k, k_stride = _rows(key, T, hkv, d, dev, "key")
+    v, v_stride = _rows(value, T, hkv, d, dev, "value")
+    ws, ws_bytes = _workspace(workspace, dev)
+    _run(_lib.pa_prefill_packed, "pa_prefill_packed", dev, stream, q, k, v, q_stride, k_stride, v_stride,
+         _p(seq_starts, torch.int32, (S + 1,), dev, "seq_starts"), S, T, int(max_seq_len), hq, hkv, d, float(scale), ws,
+         ws_bytes, _p(out, torch.bfloat16, (T, hq, d), dev, "out"), _flag(err_flag, dev))
 
 
 def pa_wait(err_flag=None, stream=None, timeout_ms: int = 10000) -> int:

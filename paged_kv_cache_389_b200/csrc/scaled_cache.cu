@@ -19,6 +19,8 @@
 // of one block; 16 or fewer as appends produce them) for one kv head of K or of V: the
 // rows are loaded once, kept in registers through the maximum and the rounding, and
 // stored as codes, so there is one pass over the data, one launch and no atomics.
+#include <type_traits>
+
 #include <cuda_fp8.h>
 
 #include "pa_common.cuh"
@@ -31,13 +33,16 @@ constexpr unsigned kFull = 0xffffffffu;
 constexpr int kWriteWarps = 4;
 constexpr int kMinExp = -64;   // scales below 2^-64 would only keep values below 1e-16
 
-// Largest |x| (bf16 bits, sign off) of the two halves of w and m, infinities and NaN left out.
-__device__ __forceinline__ uint32_t amax2(uint32_t m, uint32_t w) {
+constexpr uint32_t kInfBits = 0x7f80;   // bf16 |x| bits from here on: infinities and NaN
+
+// Largest |x| (bf16 bits, sign off) of the two halves of w and m.
+__device__ __forceinline__ uint32_t amax2(uint32_t m, uint32_t w) { return __vmaxu2(m, w & 0x7fff7fffu); }
+
+// The same with infinities and NaN left out.
+__device__ __forceinline__ uint32_t amax2_finite(uint32_t m, uint32_t w) {
     uint32_t a = w & 0x7fff7fffu;
-    if (((a + 0x00800080u) & 0x80008000u) != 0u) {  // an exponent of all ones in one half
-        if ((a & 0x7f80u) == 0x7f80u) a &= 0xffff0000u;
-        if ((a & 0x7f800000u) == 0x7f800000u) a &= 0x0000ffffu;
-    }
+    if ((a & 0xffffu) >= kInfBits) a &= 0xffff0000u;
+    if ((a >> 16) >= kInfBits) a &= 0x0000ffffu;
     return __vmaxu2(m, a);
 }
 
@@ -67,11 +72,21 @@ __device__ __forceinline__ uint32_t encode4(float a, float b, float c, float d) 
     }
 }
 
-__device__ __forceinline__ uint32_t encode_bf16x4(uint32_t w0, uint32_t w1, float inv, bool int8) {
+// Four bf16 values -> four codes.  kFinite: no infinity or NaN among them, so that |x * inv| is
+// at most the largest code; int8 then rounds by adding 1.5 * 2^23 (x * inv is exact, so this is
+// the one rounding, to nearest even) and takes the low byte: the conversion instruction
+// runs at a quarter of that rate.
+template <bool kInt8, bool kFinite>
+__device__ __forceinline__ uint32_t encode_bf16x4(uint32_t w0, uint32_t w1, float inv) {
     const float2 a = __bfloat1622float2(*reinterpret_cast<const __nv_bfloat162 *>(&w0));
     const float2 b = __bfloat1622float2(*reinterpret_cast<const __nv_bfloat162 *>(&w1));
-    return int8 ? encode4<true>(a.x * inv, a.y * inv, b.x * inv, b.y * inv)
-                : encode4<false>(a.x * inv, a.y * inv, b.x * inv, b.y * inv);
+    if constexpr (kInt8 && kFinite) {
+        constexpr float kMagic = 12582912.f;
+        const uint32_t lo = __byte_perm(__float_as_uint(fmaf(a.x, inv, kMagic)), __float_as_uint(fmaf(a.y, inv, kMagic)), 0x0040);
+        const uint32_t hi = __byte_perm(__float_as_uint(fmaf(b.x, inv, kMagic)), __float_as_uint(fmaf(b.y, inv, kMagic)), 0x0040);
+        return __byte_perm(lo, hi, 0x5410);
+    }
+    return encode4<kInt8>(a.x * inv, a.y * inv, b.x * inv, b.y * inv);
 }
 
 // Four codes re-expressed under a larger scale: round(code * ratio).
@@ -119,8 +134,8 @@ __global__ void __launch_bounds__(kWriteWarps * 32) cache_write_scaled_kernel(co
         off = (int)(slot % kBlockSize);
         return (int)(slot / kBlockSize);
     };
-    int off;
     // lane l: token w0 - 1 + l; a run starts where the block differs from the token before
+    int off;
     const int mine = block_of(w0 - 1 + lane, off);
     const int before = __shfl_up_sync(kFull, mine, 1);
     if (rem == 0 && lane >= 1 && lane <= window && w0 - 1 + lane < T && p.slots[w0 - 1 + lane] >= num_slots)
@@ -132,6 +147,7 @@ __global__ void __launch_bounds__(kWriteWarps * 32) cache_write_scaled_kernel(co
     unsigned char *pool = static_cast<unsigned char *>(is_v ? p.pool.vc : p.pool.kc);
     float *scales = is_v ? p.pool.vs : p.pool.ks;
     const int c = lane % kLanes, r0 = lane / kLanes;
+    const unsigned char *base = src + (int64_t)h * D * 2 + c * 16;
 
     while (leaders) {
         const int l = __ffs(leaders) - 1;
@@ -140,75 +156,98 @@ __global__ void __launch_bounds__(kWriteWarps * 32) cache_write_scaled_kernel(co
         const int blk = __shfl_sync(kFull, mine, l);
         const int64_t bh = (int64_t)blk * hkv + h;
         const float old_scale = scales[bh];
-        // the run's length and the slots it writes
-        int n = 0;
-        uint32_t written = 0;
-        for (;;) {
+        // The run's length and the slots it writes, from the entries this warp holds (16
+        // tokens from any leader on); a run that reaches the last of them (more than 16 tokens:
+        // slots named twice) is followed through the mapping.
+        const unsigned same = __ballot_sync(kFull, mine == blk) >> l;
+        int n = ~same == 0u ? 32 : __ffs(~same) - 1;
+        uint32_t written = __reduce_or_sync(kFull, lane >= l && lane < l + n ? 1u << off : 0u);
+        bool more = l + n >= 32;
+        while (more) {
             int o;
-            const bool same = block_of(i0 + n + lane, o) == blk;
-            const unsigned m = __ballot_sync(kFull, same);
+            const bool go = block_of(i0 + n + lane, o) == blk;
+            const unsigned m = __ballot_sync(kFull, go);
             const int k = m == kFull ? 32 : __ffs(~m) - 1;
             written |= __reduce_or_sync(kFull, lane < k ? 1u << o : 0u);
             n += k;
-            if (k < 32) break;
+            more = k == 32;
         }
         // pass 1: the rows, 16 at a time (the last 16 stay in registers), and their maximum
         uint4 row[kPasses];
         uint32_t am = 0;
-        const unsigned char *base = src + (int64_t)h * D * 2 + c * 16;
         auto load = [&](int first) {
 #pragma unroll
             for (int k = 0; k < kPasses; ++k) {
                 const int t = first + k * kRows + r0;
                 row[k] = make_uint4(0, 0, 0, 0);
-                if (t < n) row[k] = *reinterpret_cast<const uint4 *>(base + (int64_t)(i0 + t) * stride);
+                if (t < n) row[k] = __ldg(reinterpret_cast<const uint4 *>(base + (int64_t)(i0 + t) * stride));
             }
         };
-        int first = 0;
-        for (; first < n; first += kBlockSize) {
+        for (int first = 0; first < n; first += kBlockSize) {
             load(first);
 #pragma unroll
             for (int k = 0; k < kPasses; ++k) am = amax2(amax2(amax2(amax2(am, row[k].x), row[k].y), row[k].z), row[k].w);
         }
-        const uint32_t a16 = __reduce_max_sync(kFull, max(am & 0xffffu, am >> 16));
+        uint32_t a16 = __reduce_max_sync(kFull, max(am & 0xffffu, am >> 16));
+        const bool finite = a16 < kInfBits;
+        if (!finite) {   // once more without the infinities and NaN
+            am = 0;
+            for (int first = 0; first < n; first += kBlockSize) {
+                if (n > kBlockSize) load(first);
+#pragma unroll
+                for (int k = 0; k < kPasses; ++k)
+                    am = amax2_finite(amax2_finite(amax2_finite(amax2_finite(am, row[k].x), row[k].y), row[k].z), row[k].w);
+            }
+            a16 = __reduce_max_sync(kFull, max(am & 0xffffu, am >> 16));
+        }
         const int e_new = scale_exp<kInt8>(a16);
         const bool fresh = (written & 1u) != 0u;
         // a stored scale that is no finite positive number counts as none
         const bool has_old = !fresh && old_scale > 0.f && old_scale < INFINITY;
         float sigma = exp2_int(e_new);
         if (has_old && old_scale > sigma) sigma = old_scale;
+        unsigned char *block = pool + bh * (kBlockSize * D) + c * 8;
         // earlier tokens of the block under the larger scale
         if (has_old && sigma > old_scale) {
             const float ratio = old_scale / sigma;
             const uint32_t below = (2u << (31 - __clz(written))) - 1u;
-            uint32_t keep = below & ~written;
-            unsigned char *b0 = pool + bh * (kBlockSize * D) + c * 8;
+            const uint32_t keep = below & ~written;
+            uint2 held[kPasses];
 #pragma unroll
             for (int k = 0; k < kPasses; ++k) {
                 const int o = k * kRows + r0;
-                if (keep >> o & 1u) {
-                    uint2 *at = reinterpret_cast<uint2 *>(b0 + o * D);
-                    const uint2 w = *at;
-                    *at = make_uint2(recode4<kInt8>(w.x, ratio), recode4<kInt8>(w.y, ratio));
-                }
+                if (keep >> o & 1u) held[k] = *reinterpret_cast<const uint2 *>(block + o * D);
+            }
+#pragma unroll
+            for (int k = 0; k < kPasses; ++k) {
+                const int o = k * kRows + r0;
+                if (keep >> o & 1u)
+                    *reinterpret_cast<uint2 *>(block + o * D) =
+                        make_uint2(recode4<kInt8>(held[k].x, ratio), recode4<kInt8>(held[k].y, ratio));
             }
         }
         if (lane == 0 && !(has_old && sigma == old_scale)) scales[bh] = sigma;
         // pass 2: the codes (rows of runs beyond 16 tokens are loaded again)
         const float inv = 1.f / sigma;
-        for (int f = 0; f < n; f += kBlockSize) {
-            if (n > kBlockSize) load(f);
+        auto store = [&](auto all_finite) {
+            constexpr bool kFin = decltype(all_finite)::value;
+            for (int f = 0; f < n; f += kBlockSize) {
+                if (n > kBlockSize) load(f);
 #pragma unroll
-            for (int k = 0; k < kPasses; ++k) {
-                const int t = f + k * kRows + r0;
-                if (t < n) {
-                    const int o = (int)(p.slots[i0 + t] % kBlockSize);
-                    *reinterpret_cast<uint2 *>(pool + bh * (kBlockSize * D) + o * D + c * 8) =
-                        make_uint2(encode_bf16x4(row[k].x, row[k].y, inv, kInt8),
-                                   encode_bf16x4(row[k].z, row[k].w, inv, kInt8));
+                for (int k = 0; k < kPasses; ++k) {
+                    const int t = f + k * kRows + r0;
+                    // the token's offset in the block: held by lane l + t unless the run is a long one
+                    int o = __shfl_sync(kFull, off, (l + t) & 31);
+                    if (n > kBlockSize && t < n) o = (int)(p.slots[i0 + t] % kBlockSize);
+                    if (t < n)
+                        *reinterpret_cast<uint2 *>(block + o * D) =
+                            make_uint2(encode_bf16x4<kInt8, kFin>(row[k].x, row[k].y, inv),
+                                       encode_bf16x4<kInt8, kFin>(row[k].z, row[k].w, inv));
                 }
             }
-        }
+        };
+        if (finite) store(std::true_type{});
+        else store(std::false_type{});
         __syncwarp();
     }
 }

@@ -21,12 +21,15 @@
 //    longer than another, few long contexts fill the GPU as many short ones do, and the
 //    cut is computed on the device from the lengths (a captured graph follows them).
 //  * A warp streams its blocks through a ring of its own (16-byte cp.async, the next
-//    blocks and their scales in flight while one is computed): 16 warps with 8 KB each
-//    are 128 KB in flight per SM; nothing is shared between warps while they stream.
+//    blocks and their scales in flight while one is computed): 12 warps with 8 KB each
+//    are 96 KB in flight per SM; nothing is shared between warps while they stream.  (16 warps of
+//    128 registers or a third stage only lengthened the queue to memory: 200 and 201 us
+//    against 193 for 256 lognormal contexts, 1.08 GB.)
 //  * A segment that lies within one warp's items is written out at once.  Parts of
 //    segments at the ends of a warp's items meet in shared memory when the CTA's warps
 //    are done, and only parts at the ends of a CTA's items go through the workspace (two
-//    per CTA, whatever the context) to a second kernel.
+//    per CTA, whatever the context) to a second kernel.  Where all contexts are short, CTAs
+//    take whole segments and there is no second kernel.
 //  * QK^T as S^T = K Q^T and PV as O^T = V^T W^T on m16n8k16 f16 tiles with the
 //    block's 16 tokens (or 16 head dims) in M and the g heads in N: each thread reads
 //    whole 16-byte pieces of the code rows and widens them in registers.
@@ -44,11 +47,12 @@ namespace {
 
 constexpr unsigned kFull = 0xffffffffu;
 constexpr float kLog2e = 1.4426950408889634f;
-constexpr int kWarps = 16;
+constexpr int kWarps = 12;
 constexpr int kThreads = kWarps * 32;
 constexpr float kLazy = 256.f;        // p and w may grow to 2^8 before the reference points move
 constexpr int kMaxCum = 8192;         // prefix-sum entries in shared memory (every k-th sequence beyond)
 constexpr int kMinItems = 2;          // items a warp takes at least (fewer CTAs for tiny batches)
+constexpr int kWholeItems = 33;       // longest segments that stay within a CTA
 constexpr int kMergeThreads = 256;
 
 template <int D, int G>
@@ -79,6 +83,7 @@ struct Params {
     int32_t *err;
     int32_t max_blocks, max_context, num_seqs, num_q_heads, num_kv_heads, num_blocks;
     int32_t cum_step;        // sequences per prefix-sum entry
+    bool whole;              // CTAs take whole segments: nothing to join afterwards
     float scale_log2;
 };
 
@@ -178,19 +183,26 @@ __device__ __forceinline__ void load_q(const Params &p, int s, int h, State<D> &
     for (int k = 0; k < 2; ++k) st.c[k] = p.scale_log2 * __shfl_sync(kFull, up, (2 * t + k) * 4);
 }
 
-// One 16-token block (ntok >= 1 of them in the context).
-template <int D, bool kInt8>
-__device__ __forceinline__ void block_step(unsigned char *stage, int ntok, State<D> &st, int lane) {
+__device__ __forceinline__ float fmax3(float a, float b, float c) {
+    float r;
+    asm("max.f32 %0, %1, %2, %3;" : "=f"(r) : "f"(a), "f"(b), "f"(c));
+    return r;
+}
+
+// One 16-token block; kTail: only ntok (1 .. 15) of them are in the context.
+template <int D, bool kInt8, bool kTail>
+__device__ __forceinline__ void block_step(unsigned char *stage, const float2 sc, int ntok, State<D> &st, int lane) {
     constexpr int kSlab = kBlockSize * D;
     constexpr int kVBytes = D / 8;   // bytes of a V row per thread
     const int g = lane >> 2, t = lane & 3;
-    const float2 sc = *reinterpret_cast<const float2 *>(stage + 2 * kSlab);
-    float sa[4] = {0.f, 0.f, 0.f, 0.f}, sb[4] = {0.f, 0.f, 0.f, 0.f};
+    float sx[4][4] = {};   // four chains of k steps
 #pragma unroll
     for (int j = 0; j < D / 64; ++j) {
         const int ch = (D / 64) * t + j;
-        const uint4 lo = *reinterpret_cast<const uint4 *>(stage + g * D + ((ch ^ swz<D>(g)) << 4));
-        const uint4 hi = *reinterpret_cast<const uint4 *>(stage + (g + 8) * D + ((ch ^ swz<D>(g + 8)) << 4));
+        // swz(g + 8) == swz(g)
+        const unsigned char *row = stage + g * D + ((ch ^ swz<D>(g)) << 4);
+        const uint4 lo = *reinterpret_cast<const uint4 *>(row);
+        const uint4 hi = *reinterpret_cast<const uint4 *>(row + 8 * D);
         const uint32_t wl[4] = {lo.x, lo.y, lo.z, lo.w}, wh[4] = {hi.x, hi.y, hi.z, hi.w};
 #pragma unroll
         for (int i = 0; i < 4; ++i) {
@@ -198,36 +210,47 @@ __device__ __forceinline__ void block_step(unsigned char *stage, int ntok, State
             uint32_t a[4];
             widen4<kInt8>(wl[i], a[0], a[2]);
             widen4<kInt8>(wh[i], a[1], a[3]);
-            if (kk & 1) mma_f16_16816(sb, a, st.q[kk][0], st.q[kk][1]);
-            else mma_f16_16816(sa, a, st.q[kk][0], st.q[kk][1]);
+            mma_f16_16816(sx[kk & 3], a, st.q[kk][0], st.q[kk][1]);
         }
     }
     float s[4], pr[4], w[4];
     const float c0 = st.c[0] * sc.x, c1 = st.c[1] * sc.x;
-    s[0] = (sa[0] + sb[0]) * c0;
-    s[1] = (sa[1] + sb[1]) * c1;
-    s[2] = (sa[2] + sb[2]) * c0;
-    s[3] = (sa[3] + sb[3]) * c1;
-    if (ntok < kBlockSize) {
-        if (g >= ntok) s[0] = s[1] = -INFINITY;
-        if (g + 8 >= ntok) s[2] = s[3] = -INFINITY;
+#pragma unroll
+    for (int i = 0; i < 4; ++i) s[i] = (sx[0][i] + sx[1][i]) + (sx[2][i] + sx[3][i]);
+    if constexpr (kTail) {
+        // a masked score is -inf whatever the sign of the factor
+        const float n0 = c0 < 0.f ? INFINITY : -INFINITY, n1 = c1 < 0.f ? INFINITY : -INFINITY;
+        if (g >= ntok) s[0] = n0, s[1] = n1;
+        if (g + 8 >= ntok) s[2] = n0, s[3] = n1;
     }
     auto weights = [&]() -> bool {
         const float f0 = sc.y * st.gf[0], f1 = sc.y * st.gf[1];
 #pragma unroll
-        for (int i = 0; i < 4; ++i) pr[i] = fast_exp2(s[i] - st.m[i & 1]);
+        for (int i = 0; i < 4; ++i) pr[i] = fast_exp2(fmaf(s[i], i & 1 ? c1 : c0, -st.m[i & 1]));
+        if constexpr (kTail) {   // a factor of zero would make the masked ones NaN
+            if (g >= ntok) pr[0] = pr[1] = 0.f;
+            if (g + 8 >= ntok) pr[2] = pr[3] = 0.f;
+        }
         w[0] = pr[0] * f0;
         w[1] = pr[1] * f1;
         w[2] = pr[2] * f0;
         w[3] = pr[3] * f1;
-        const float a = fmaxf(fmaxf(pr[0], pr[2]), fmaxf(w[0], w[2]));
-        const float b = fmaxf(fmaxf(pr[1], pr[3]), fmaxf(w[1], w[3]));
-        return fmaxf(a, b) <= kLazy;
+        const float a = fmax3(fmax3(pr[0], pr[1], pr[2]), pr[3], w[0]);
+        return fmax3(fmax3(a, w[1], w[2]), w[3], 0.f) <= kLazy;
     };
-    const bool fine = st.m[0] != -INFINITY && weights();
+    // m is -inf until the first block: the exponentials are then infinite or NaN
+    const bool fine = weights() && st.m[0] != -INFINITY;
     if (!__all_sync(kFull, fine)) {
         // move the reference points: the largest score so far, and the largest score plus log2(sigma_v)
-        float x0 = fmaxf(s[0], s[2]), x1 = fmaxf(s[1], s[3]);
+        float x0 = -INFINITY, x1 = -INFINITY;
+        if (!kTail || g < ntok) {
+            x0 = s[0] * c0;
+            x1 = s[1] * c1;
+        }
+        if (!kTail || g + 8 < ntok) {
+            x0 = fmaxf(x0, s[2] * c0);
+            x1 = fmaxf(x1, s[3] * c1);
+        }
 #pragma unroll
         for (int off = 4; off < 32; off <<= 1) {
             x0 = fmaxf(x0, __shfl_xor_sync(kFull, x0, off));
@@ -235,17 +258,17 @@ __device__ __forceinline__ void block_step(unsigned char *stage, int ntok, State
         }
         const float lv = fmaxf(__log2f(sc.y), -126.f);
         const float x[2] = {x0, x1};
-        float al[2], ao[2];
+        float ao[2];
 #pragma unroll
         for (int k = 0; k < 2; ++k) {
             const float m = fmaxf(st.m[k], x[k]), mo = fmaxf(st.mo[k], x[k] + lv);
-            al[k] = st.m[k] == -INFINITY ? 0.f : fast_exp2(st.m[k] - m);
+            const float al = st.m[k] == -INFINITY ? 0.f : fast_exp2(st.m[k] - m);
             ao[k] = st.mo[k] == -INFINITY ? 0.f : fast_exp2(st.mo[k] - mo);
             // no finite score yet: any finite reference will do
             st.m[k] = m == -INFINITY ? -FLT_MAX : m;
             st.mo[k] = m == -INFINITY ? -FLT_MAX : mo;
             st.gf[k] = fast_exp2(st.m[k] - st.mo[k]);
-            st.l[k] *= al[k];
+            st.l[k] *= al;
         }
 #pragma unroll
         for (int mt = 0; mt < D / 16; ++mt) {
@@ -261,7 +284,7 @@ __device__ __forceinline__ void block_step(unsigned char *stage, int ntok, State
     const uint32_t pb0 = movmatrix_trans(pack_f16x2(w[0], w[1]));
     const uint32_t pb1 = movmatrix_trans(pack_f16x2(w[2], w[3]));
     unsigned char *vb = stage + kSlab;
-    if (ntok < kBlockSize) {
+    if constexpr (kTail) {
         // codes past the context may stand for NaN: zero those rows
         for (int i = lane; i < (kBlockSize - ntok) * (D / 16); i += 32)
             *reinterpret_cast<uint4 *>(vb + (ntok + i / (D / 16)) * D + (i % (D / 16)) * 16) = make_uint4(0, 0, 0, 0);
@@ -485,12 +508,23 @@ __global__ void __launch_bounds__(kThreads, 1) decode_scaled_kernel(const __grid
     const int64_t total = (int64_t)cum[ncum] * hkv;
     const int64_t workers = (int64_t)gridDim.x * kWarps;
     const int64_t per = max((int64_t)kMinItems, (total + workers - 1) / workers);
-    const int64_t cta0 = min(total, (int64_t)blockIdx.x * kWarps * per), cta1 = min(total, cta0 + kWarps * per);
+    int64_t cta0 = min(total, (int64_t)blockIdx.x * kWarps * per), cta1 = min(total, cta0 + kWarps * per);
+    int64_t warp_items = per;
+    if (p.whole) {   // both ends move up to where a segment begins
+        auto up = [&](int64_t x) -> int64_t {
+            if (x >= total) return total;
+            const Place pl = place_of(p, cum, ncum, x);
+            return pl.b == 0 ? x : x - pl.b + pl.nb + 1;
+        };
+        cta0 = up(cta0);
+        cta1 = up(cta1);
+        warp_items = (cta1 - cta0 + kWarps - 1) / kWarps;
+    }
     if (cta0 >= cta1) {
-        if (threadIdx.x == 0) p.tails[blockIdx.x] = make_int4(-1, 0, 0, 0);
+        if (threadIdx.x == 0 && !p.whole) p.tails[blockIdx.x] = make_int4(-1, 0, 0, 0);
         return;
     }
-    const int64_t w0 = min(cta1, cta0 + warp * per), w1 = min(cta1, w0 + per);
+    const int64_t w0 = min(cta1, cta0 + warp * warp_items), w1 = min(cta1, w0 + warp_items);
     int seg_a = -1, seg_b = -1;  // segments of this warp's first and last parts
     unsigned char *part_a = smem + L::kOffA + (size_t)warp * L::kPiece;
     State<D> st;
@@ -498,6 +532,8 @@ __global__ void __launch_bounds__(kThreads, 1) decode_scaled_kernel(const __grid
     if (w0 < w1) {
         unsigned char *ring = smem + (size_t)warp * L::kStages * L::kStage;
         const uint32_t ring_s = smem_u32(ring);
+        constexpr int kPerRow = D / 16;   // 16-byte chunks of a row
+        const uint32_t lane_off = (uint32_t)((lane / kPerRow) * D + (((lane % kPerRow) ^ swz<D>(lane / kPerRow)) << 4));
         // The fetch cursor: item by item over the warp's blocks.  Lane i of `ent` holds the
         // table entry of block eb + i of its segment; `nxt` those of the 32 after them, or of
         // the next segment's first 32.
@@ -547,15 +583,15 @@ __global__ void __launch_bounds__(kThreads, 1) decode_scaled_kernel(const __grid
                 const bool ok = blk >= 0 && blk < p.num_blocks;
                 if (ok) {
                     const int64_t bh = (int64_t)blk * hkv + fp.h;
-                    const unsigned char *ks = p.kc + bh * L::kSlab, *vs = p.vc + bh * L::kSlab;
+                    const unsigned char *ks = p.kc + bh * L::kSlab + lane * 16, *vs = p.vc + bh * L::kSlab + lane * 16;
                     const uint32_t dst = ring_s + stage * L::kStage;
-                    constexpr int kChunks = L::kSlab / 16, kPerRow = D / 16;
 #pragma unroll
-                    for (int i = 0; i < kChunks / 32; ++i) {
-                        const int ch = i * 32 + lane, r = ch / kPerRow, c = ch % kPerRow;
-                        const uint32_t at = dst + r * D + ((c ^ swz<D>(r)) << 4);
-                        cp_async16(at, ks + ch * 16);
-                        cp_async16(at + L::kSlab, vs + ch * 16);
+                    for (int i = 0; i < L::kSlab / 512; ++i) {
+                        // chunk 32 i + lane is in row i * (512 / D) + lane / (D / 16): the row's part of the
+                        // swizzle that i sets is bit 2 (d = 128) or none (d = 64)
+                        const uint32_t at = dst + i * 512 + (D == 128 && (i & 1) ? lane_off ^ 64u : lane_off);
+                        cp_async16(at, ks + i * 512);
+                        cp_async16(at + L::kSlab, vs + i * 512);
                     }
                     if (lane < 2) cp_async4(dst + 2 * L::kSlab + lane * 4, (lane == 0 ? p.ks : p.vs) + bh);
                 } else if (lane == 0) {
@@ -582,12 +618,17 @@ __global__ void __launch_bounds__(kThreads, 1) decode_scaled_kernel(const __grid
             const bool ends = cp.nb - cp.b < w1 - ci;                       // the empty item too
             const bool whole = cp.b == 0 && ends;
             if (b_end > cp.b) load_q<D, G>(p, cp.s, cp.h, st, lane);
+            const int b_tail = len % kBlockSize != 0 ? cp.nb - 1 : INT_MAX;   // the partly filled block
             for (int b = cp.b; b < b_end; ++b) {
                 cp_async_wait_dyn(n_iss - n_cmp - 1);
                 __syncwarp();
                 const int stage = n_cmp % L::kStages;
-                if (okmask >> stage & 1u)
-                    block_step<D, kInt8>(ring + stage * L::kStage, min(kBlockSize, len - b * kBlockSize), st, lane);
+                if (okmask >> stage & 1u) {
+                    unsigned char *at = ring + stage * L::kStage;
+                    const float2 sc = *reinterpret_cast<const float2 *>(at + 2 * L::kSlab);
+                    if (b != b_tail) block_step<D, kInt8, false>(at, sc, kBlockSize, st, lane);
+                    else block_step<D, kInt8, true>(at, sc, len - b * kBlockSize, st, lane);
+                }
                 __syncwarp();
                 ++n_cmp;
                 fetch_one();
@@ -615,8 +656,8 @@ __global__ void __launch_bounds__(kThreads, 1) decode_scaled_kernel(const __grid
     __syncthreads();
     // ---- the CTA's parts: runs of one segment, joined; those that reach beyond the
     // CTA's items go to the workspace
-    const int mine = segs[lane];   // 2 * kWarps == 32 parts in item order
-    static_assert(2 * kWarps == 32, "one lane per part");
+    const int mine = lane < 2 * kWarps ? segs[lane] : -1;   // parts in item order
+    static_assert(2 * kWarps <= 32, "one lane per part");
     const unsigned have = __ballot_sync(kFull, mine >= 0);
     const unsigned before = have & ((1u << lane) - 1u);
     const int prev = __shfl_sync(kFull, mine, before ? 31 - __clz(before) : lane);
@@ -668,6 +709,7 @@ __global__ void __launch_bounds__(kThreads, 1) decode_scaled_kernel(const __grid
             }
         }
     }
+    if (p.whole) return;
     // exactly one warp writes the CTA's tail record
     if (!__syncthreads_or(tail) && threadIdx.x == 0) p.tails[blockIdx.x] = make_int4(-1, 0, 0, 0);
 }
@@ -706,8 +748,12 @@ cudaError_t launch(Params &p, void *workspace, int ctas, cudaStream_t stream) {
     cudaError_t e = cudaFuncSetAttribute(decode_scaled_kernel<D, G, kInt8>, cudaFuncAttributeMaxDynamicSharedMemorySize,
                                          (int)L::bytes(kMaxCum + 1));
     if (e != cudaSuccess) return e;
+    // Segments of at most kWholeItems items (496 tokens) stay within a CTA, which costs a CTA
+    // at most one segment more than its share and saves the second kernel (four
+    // sequences of 17 to 100 tokens: 9.1 us against 9.6 in a graph).
+    p.whole = p.max_context / kBlockSize + 2 <= kWholeItems;
     decode_scaled_kernel<D, G, kInt8><<<(unsigned)ctas, kThreads, L::bytes(ncum + 1), stream>>>(p);
-    if ((e = cudaGetLastError()) != cudaSuccess) return e;
+    if ((e = cudaGetLastError()) != cudaSuccess || p.whole) return e;
     return launch_after(join_scaled_kernel<D, G>, dim3((unsigned)ctas), dim3(kMergeThreads), 0, stream,
                         static_cast<const Params &>(p));
 }
