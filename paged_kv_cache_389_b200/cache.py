@@ -1,8 +1,9 @@
 """PagedKVCache: one layer's K/V pool on the GPU plus the host block manager.
 
 Orchestration only: the host C++ BlockManager decides slots, tables and copy
-pairs; pa_copy_blocks / pa_cache_write / pa_decode / pa_prefill_chunk do all the
-device work.  Order within a step follows the pages' data flow (a new token is
+pairs; pa_copy_blocks / pa_cache_write / pa_decode / pa_prefill_chunk (for a pool
+with a scale per block and kv head pa_copy_blocks_scaled / pa_cache_write_scaled /
+pa_decode_scaled) and pa_prefill_packed do all the device work.  Order within a step follows the pages' data flow (a new token is
 written back into the cache, then attended to): copy-on-write copies, then the
 cache write, then attention, all on one stream.
 """
@@ -12,8 +13,9 @@ import math
 
 import numpy as np
 
-from . import (BlockManager, pa_cache_write, pa_copy_blocks, pa_decode, pa_decode_workspace_size,
-               pa_prefill_chunk, BLOCK_SIZE)
+from . import (BlockManager, pa_cache_write, pa_cache_write_scaled, pa_copy_blocks, pa_copy_blocks_scaled, pa_decode,
+               pa_decode_scaled, pa_decode_scaled_workspace_size, pa_decode_workspace_size, pa_prefill_chunk,
+               pa_prefill_packed, pa_prefill_packed_workspace_size, BLOCK_SIZE)
 
 
 def _torch():
@@ -23,23 +25,38 @@ def _torch():
 
 class PagedKVCache:
     def __init__(self, num_blocks: int, num_kv_heads: int, head_dim: int, dtype, device="cuda",
-                 free_order=None, fill_nan: bool = True, k_scale: float = 1.0, v_scale: float = 1.0):
+                 free_order=None, fill_nan: bool = True, k_scale: float = 1.0, v_scale: float = 1.0,
+                 block_scales: bool = False):
         """dtype torch.float32, torch.bfloat16 or torch.float8_e4m3fn; an fp8 pool stores
-        e4m3(x / k_scale) and e4m3(x / v_scale) and takes bf16 queries and K/V."""
+        e4m3(x / k_scale) and e4m3(x / v_scale) and takes bf16 queries and K/V.  With
+        block_scales, dtype torch.float8_e4m3fn or torch.int8: every (block, kv head) has
+        a power-of-two scale of its own that follows the data (nothing to calibrate)."""
         torch = _torch()
         self.num_blocks, self.num_kv_heads, self.head_dim = num_blocks, num_kv_heads, head_dim
         self.dtype, self.device = dtype, torch.device(device)
         self.k_scale, self.v_scale = float(k_scale), float(v_scale)
+        self.block_scales = bool(block_scales)
         shape = (num_blocks, num_kv_heads, BLOCK_SIZE, head_dim)
+        if dtype == torch.int8 and not block_scales:
+            raise ValueError("int8 pools have a scale per block and kv head: block_scales=True")
+        if block_scales and dtype not in (torch.int8, torch.float8_e4m3fn):
+            raise ValueError("block_scales: torch.float8_e4m3fn or torch.int8 pools")
         # NaN in every slot nothing has written: a stray read poisons the output
         if dtype == torch.float8_e4m3fn:
             code = 0x7F if fill_nan else 0x00          # e4m3 NaN / +0
             self.key_cache = torch.full(shape, code, dtype=torch.uint8, device=self.device).view(dtype)
             self.value_cache = torch.full(shape, code, dtype=torch.uint8, device=self.device).view(dtype)
+        elif dtype == torch.int8:
+            self.key_cache = torch.zeros(shape, dtype=dtype, device=self.device)
+            self.value_cache = torch.zeros(shape, dtype=dtype, device=self.device)
         else:
             fill = float("nan") if fill_nan else 0.0
             self.key_cache = torch.full(shape, fill, dtype=dtype, device=self.device)
             self.value_cache = torch.full(shape, fill, dtype=dtype, device=self.device)
+        if block_scales:
+            fill = float("nan") if fill_nan else 0.0
+            self.key_scales = torch.full(shape[:2], fill, dtype=torch.float32, device=self.device)
+            self.value_scales = torch.full(shape[:2], fill, dtype=torch.float32, device=self.device)
         self.manager = BlockManager(num_blocks, BLOCK_SIZE, free_order)
         self.err_flag = torch.zeros(1, dtype=torch.int32, device=self.device)
 
@@ -64,11 +81,20 @@ class PagedKVCache:
         """Copy-on-write copies (if any), then scatter k/v [T, Hkv, d] into ``slots``."""
         torch = _torch()
         if pairs is not None and len(pairs):
-            pa_copy_blocks(self.key_cache, self.value_cache, torch.as_tensor(pairs, device=self.device),
-                           self.err_flag, stream)
+            pairs = torch.as_tensor(pairs, device=self.device)
+            if self.block_scales:
+                pa_copy_blocks_scaled(self.key_cache, self.value_cache, self.key_scales, self.value_scales, pairs,
+                                      self.err_flag, stream)
+            else:
+                pa_copy_blocks(self.key_cache, self.value_cache, pairs, self.err_flag, stream)
         if len(slots):
-            pa_cache_write(k, v, torch.as_tensor(slots, device=self.device), self.key_cache,
-                           self.value_cache, self.err_flag, stream, self.k_scale, self.v_scale)
+            slots = torch.as_tensor(slots, device=self.device)
+            if self.block_scales:
+                pa_cache_write_scaled(k, v, slots, self.key_cache, self.value_cache, self.key_scales, self.value_scales,
+                                      self.err_flag, stream)
+            else:
+                pa_cache_write(k, v, slots, self.key_cache, self.value_cache, self.err_flag, stream, self.k_scale,
+                               self.v_scale)
 
     def append(self, seqs, k, v, counts=None, stream=None):
         slots, pairs = self.plan_append(seqs, counts)
@@ -89,11 +115,45 @@ class PagedKVCache:
         tables, lens, max_len = self.tables(seqs, max_blocks)
         max_len = max(max_len, 1)
         out = torch.empty_like(q) if out is None else out
+        if self.block_scales:    # the context is always split: partition_size says nothing here
+            if workspace is None:
+                workspace = self._scratch(pa_decode_scaled_workspace_size(q.shape[1], self.num_kv_heads, q.shape[2]), stream)
+            pa_decode_scaled(q, self.key_cache, self.value_cache, self.key_scales, self.value_scales, tables, lens, max_len,
+                             scale, out, workspace, self.err_flag, stream)
+            return out
         if partition_size and workspace is None:
             ws = pa_decode_workspace_size(len(seqs), q.shape[1], q.shape[2], max_len, partition_size)
             workspace = torch.empty(max(ws, 16), dtype=torch.uint8, device=self.device)
         pa_decode(q, self.key_cache, self.value_cache, tables, lens, max_len, scale, out,
                   partition_size, workspace, self.err_flag, stream, self.k_scale, self.v_scale)
+        return out
+
+    def _scratch(self, nbytes, stream):
+        """Workspace for one call on `stream` (None: the current one)."""
+        torch = _torch()
+        ws = torch.empty(max(nbytes, 16), dtype=torch.uint8, device=self.device)
+        if stream is not None:
+            ws.record_stream(stream)
+        return ws
+
+    def prompt(self, q, k, v, seqs, counts, scale, out=None, stream=None):
+        """Whole prompts of empty sequences: causal attention over each of them and their
+        K/V appended to the cache.  q [T, Hq, d], k/v [T, Hkv, d] bf16, packed: counts[i] rows
+        of seqs[i] after those of seqs[i - 1] (their tokens may be strided).  Returns the
+        attention's output [T, Hq, d]."""
+        torch = _torch()
+        counts = [int(c) for c in counts]
+        if any(self.manager.num_tokens(s) != 0 for s in seqs):
+            raise ValueError("prompt() takes sequences without tokens; prefill() continues others")
+        if sum(counts) != q.shape[0]:
+            raise ValueError("counts must add up to the rows of q")
+        slots, pairs = self.plan_append(seqs, counts)
+        starts = torch.zeros(len(counts) + 1, dtype=torch.int32)
+        starts[1:] = torch.cumsum(torch.tensor(counts, dtype=torch.int64), 0)
+        out = torch.empty(q.shape, dtype=q.dtype, device=self.device) if out is None else out
+        ws = self._scratch(pa_prefill_packed_workspace_size(q.shape[0], len(counts), q.shape[1], self.num_kv_heads), stream)
+        pa_prefill_packed(q, k, v, starts.to(self.device), max(counts, default=0), scale, out, ws, self.err_flag, stream)
+        self.write(k if self.block_scales else k.contiguous(), v if self.block_scales else v.contiguous(), slots, pairs, stream)
         return out
 
     def prefill(self, q, seqs, chunk_lens, scale, out=None, max_blocks=None, stream=None):

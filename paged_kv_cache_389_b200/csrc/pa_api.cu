@@ -430,8 +430,9 @@ pa_status pa_decode_scaled(const void *query, const void *key_cache, const void 
     if (workspace_bytes < pa_decode_scaled_workspace_size(num_q_heads, cache->num_kv_heads, cache->head_dim))
         return PA_ERR_INVALID_ARG;
     if ((int64_t)max_context_len > (int64_t)max_blocks_per_seq * kBlockSize) return PA_ERR_INVALID_ARG;
-    // items (blocks and one more per sequence) are counted in 32 bits
+    // items (blocks and one more per sequence) and (sequence, kv head) pairs are counted in 32 bits
     if ((int64_t)num_seqs * ((int64_t)max_context_len / kBlockSize + 2) > INT32_MAX) return PA_ERR_UNSUPPORTED;
+    if ((int64_t)num_seqs * cache->num_kv_heads > INT32_MAX) return PA_ERR_UNSUPPORTED;
     a.query = query;
     a.tables = block_tables;
     a.max_blocks = max_blocks_per_seq;

@@ -1,0 +1,137 @@
+"""The serving-step operators as they are used together: plan on the GPU, attention over
+packed prompts, append into the 8-bit cache, decode steps, release -- all device-side
+state, against fp64; and PagedKVCache with a scale per block."""
+import numpy as np
+import pytest
+
+from oracle import step_ops
+from test_gpu_scaled_cache import CODES, code_dtype, to_values, torch_mod
+
+pytestmark = pytest.mark.gpu
+
+
+def rows(rng, T, h, d):
+    torch = torch_mod()
+    return torch.from_numpy(rng.standard_normal((T, h, d)).astype(np.float32)).to(torch.bfloat16).cuda()
+
+
+def f64(t):
+    return t.double().cpu().numpy()
+
+
+def within(got, ref, mass, reach, tokens):
+    far = np.abs(got - ref) - step_ops.attention_bound(ref, mass, reach, tokens)
+    assert np.isfinite(got).all() and (far <= 0).all(), f"off by {far.max():.3g} more than the bound"
+
+
+@pytest.mark.parametrize("code", CODES)
+@pytest.mark.parametrize("hq,hkv,d", [(8, 2, 128), (4, 4, 64)])
+def test_prompts_then_decode_steps(pa, code, hq, hkv, d):
+    torch = torch_mod()
+    rng = np.random.default_rng(hq)
+    S, N, mb, cap = 7, 120, 12, 600
+    z = lambda *s, dt=torch.int32: torch.zeros(*s, dtype=dt, device="cuda")
+    order = rng.permutation(N).astype(np.int32)
+    lens, tables, nf, err = z(S), torch.full((S, mb), -1, dtype=torch.int32, device="cuda"), z(1) + N, z(1)
+    free, slots, starts = torch.from_numpy(order).cuda(), z(cap, dt=torch.int64), z(S + 1)
+    kc, vc = torch.zeros(2, N, hkv, 16, d, device="cuda").to(code_dtype(code)).unbind(0)
+    kc, vc = kc.contiguous(), vc.contiguous()
+    ks, vs = torch.full((2, N, hkv), float("nan"), device="cuda").unbind(0)
+    ks, vs = ks.contiguous(), vs.contiguous()
+    kref, vref = np.zeros((N, hkv, 16, d)), np.zeros((N, hkv, 16, d))
+    ksref, vsref = np.full((N, hkv), np.nan), np.full((N, hkv), np.nan)
+    ws = torch.empty(max(pa.pa_decode_scaled_workspace_size(hq, hkv, d),
+                         pa.pa_prefill_packed_workspace_size(cap, S, hq, hkv)), dtype=torch.uint8, device="cuda")
+    scale = d ** -0.5
+    counts = [40, 1, 17, 0, 128, 16, 33]
+    for step in range(6):
+        c = torch.tensor(counts, dtype=torch.int32, device="cuda")
+        ref = step_ops.step_plan(np.array(counts), lens.cpu().numpy(), tables.cpu().numpy(), free.cpu().numpy(), int(nf), cap)
+        pa.pa_step_plan(c, lens, tables, free, nf, slots, starts, err_flag=err)
+        assert np.array_equal(tables.cpu().numpy(), ref[0]) and np.array_equal(slots.cpu().numpy(), ref[1])
+        T = cap   # the whole padded buffer, as a captured step would pass it
+        fused = rows(rng, T, hq + 2 * hkv, d)
+        q, k, v = fused.split([hq, hkv, hkv], 1)
+        if step == 0:
+            out = torch.full((T, hq, d), 7.0, dtype=torch.bfloat16, device="cuda")
+            pa.pa_prefill_packed(q, k, v, starts, 128, scale, out, ws, err)
+            o, mass, reach = step_ops.packed_attention(f64(q), f64(k), f64(v), ref[2], scale)
+            n = int(ref[2][-1])
+            within(f64(out)[:n], o[:n], mass[:n], reach[:n], (0, 2.0 ** -8, 0.0))
+            assert (out[n:] == 7).all()
+        pa.pa_cache_write_scaled(k, v, slots, kc, vc, ks, vs, err)
+        step_ops.cache_write_scaled(f64(k), ref[1], kref, ksref, code)
+        step_ops.cache_write_scaled(f64(v), ref[1], vref, vsref, code)
+        assert np.array_equal(to_values(kc), kref) and np.array_equal(to_values(vc), vref)
+        assert np.array_equal(ks.cpu().numpy(), ksref, equal_nan=True) and np.array_equal(vs.cpu().numpy(), vsref, equal_nan=True)
+        qd = rows(rng, S, hq, d)
+        out = torch.empty_like(qd)
+        pa.pa_decode_scaled(qd, kc, vc, ks, vs, tables, lens, mb * 16, scale, out, ws, err)
+        o, mass, reach = step_ops.decode_scaled(f64(qd), kref, vref, ksref, vsref, ref[0], ref[3], scale)
+        within(f64(out), o, mass, reach, (mb * 16, 2.0 ** -11, 6.0))
+        if step == 3:
+            done = torch.tensor([0, 1, 0, 0, 1, 0, 0], dtype=torch.int32, device="cuda")
+            pa.pa_step_release(done, lens, tables, free, nf, err_flag=err)
+            assert lens[1] == 0 and lens[4] == 0 and (tables[4] == -1).all()
+        counts = [1, 1, 1, 0, 1, 1, 1] if step != 3 else [1, 20, 1, 3, 50, 1, 1]
+    assert pa.pa_wait(err) == 0
+
+
+@pytest.mark.parametrize("code", CODES)
+def test_paged_cache_with_block_scales(pa, code):
+    """Prompts, a fork with copy on write, and decode steps through PagedKVCache."""
+    from paged_kv_cache_389_b200.cache import PagedKVCache
+    torch = torch_mod()
+    rng = np.random.default_rng(3)
+    hq, hkv, d, scale = 8, 4, 64, 0.125
+    kv = PagedKVCache(64, hkv, d, code_dtype(code), block_scales=True)
+    assert kv.key_scales.shape == (64, hkv) and torch.isnan(kv.key_scales).all()
+    for s in (0, 1):
+        kv.add_seq(s)
+    counts = [37, 60]
+    q, k, v = rows(rng, 97, hq + 2 * hkv, d).split([hq, hkv, hkv], 1)
+    out = kv.prompt(q, k, v, [0, 1], counts, scale)
+    o, mass, reach = step_ops.packed_attention(f64(q), f64(k), f64(v), np.array([0, 37, 97]), scale)
+    within(f64(out), o, mass, reach, (0, 2.0 ** -8, 0.0))
+    with pytest.raises(ValueError):
+        kv.prompt(q, k, v, [0, 1], counts, scale)
+    kv.fork(0, 2)
+    for _ in range(3):
+        kn, vn, qn = rows(rng, 3, hkv, d), rows(rng, 3, hkv, d), rows(rng, 3, hq, d)
+        slots, pairs = kv.append([0, 1, 2], kn, vn)
+        got = kv.decode(qn, [0, 1, 2], scale)
+        t, l = kv.manager.build_tables([0, 1, 2], 8)
+        o, mass, reach = step_ops.decode_scaled(f64(qn), to_values(kv.key_cache), to_values(kv.value_cache),
+                                                kv.key_scales.cpu().numpy(), kv.value_scales.cpu().numpy(), t, l, scale)
+        within(f64(got), o, mass, reach, (64, 2.0 ** -11, 6.0))
+    # what the cache holds is what was appended, to half a step of each block's scale
+    b = kv.manager.block_table(0)
+    held = np.concatenate([to_values(kv.key_cache[x:x + 1])[0] * kv.key_scales[x].cpu().numpy()[:, None, None] for x in b[:2]], 1)
+    kk = f64(k)[:32].transpose(1, 0, 2)
+    step = np.repeat(np.stack([kv.key_scales[x].cpu().numpy() for x in b[:2]], 1), 16, 1)[:, :, None]
+    half = 0.5 * step if code == "int8" else np.maximum(2.0 ** -4 * np.abs(kk), 2.0 ** -10 * step)
+    assert (np.abs(held - kk) <= half).all()
+    assert pa.pa_wait(kv.err_flag) == 0
+
+
+def test_prompt_on_a_bf16_cache(pa):
+    """prompt() over a bf16 pool: the same attention as the chunked prefill of the same tokens."""
+    from paged_kv_cache_389_b200.cache import PagedKVCache
+    torch = torch_mod()
+    rng = np.random.default_rng(5)
+    kv = PagedKVCache(64, 2, 128, torch.bfloat16)
+    kv.add_seq(0)
+    kv.add_seq(1)
+    q, k, v = rows(rng, 150, 12, 128).split([8, 2, 2], 1)
+    side = torch.cuda.Stream()
+    torch.cuda.synchronize()
+    out = kv.prompt(q, k, v, [0, 1], [100, 50], 0.09, stream=side)
+    side.synchronize()
+    padded = torch.zeros(2, 100, 8, 128, dtype=torch.bfloat16, device="cuda")
+    padded[0], padded[1, :50] = q[:100], q[100:]
+    chunk = kv.prefill(padded, [0, 1], [100, 50], 0.09)
+    # both are off by at most their own rounding and that of P (2^-8 each) of the same attention
+    o, mass, reach = step_ops.packed_attention(f64(q), f64(k), f64(v), np.array([0, 100, 150]), 0.09)
+    within(f64(out), o, mass, reach, (0, 2.0 ** -8, 0.0))
+    within(np.concatenate([f64(chunk[0]), f64(chunk[1, :50])]), o, mass, reach, (0, 2.0 ** -8, 0.0))
+    assert pa.pa_wait(kv.err_flag) == 0

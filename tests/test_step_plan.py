@@ -215,3 +215,12 @@ def test_release(pa, S, mb):
         assert pa.pa_wait(err) == pa.PA_DEVERR_PLAN
         assert np.array_equal(td.cpu().numpy(), tables) and int(new_nf) == 4
         assert np.array_equal(new_l.cpu().numpy(), lens) and np.array_equal(fd.cpu().numpy(), free[:h - 1])
+
+
+def test_paged_cache_refuses_int8_without_block_scales(pa):
+    from paged_kv_cache_389_b200.cache import PagedKVCache
+    torch = torch_mod()
+    with pytest.raises(ValueError):
+        PagedKVCache(4, 2, 64, torch.int8, device="cpu")
+    with pytest.raises(ValueError):
+        PagedKVCache(4, 2, 64, torch.bfloat16, device="cpu", block_scales=True)
