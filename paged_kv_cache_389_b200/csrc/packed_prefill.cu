@@ -150,26 +150,33 @@ struct PlanParams {
 constexpr int kPlanThreads = 1024;
 constexpr int kBuckets = 256;
 
+// Sums of pairs stop here: starts that go back and forth can name far more than 2^31 of
+// them, and such a list has to read as too long, not as a short one.
+constexpr int kManyPairs = INT32_MAX / 2;
+__device__ __forceinline__ int add_pairs(int a, int b) { return min(a + b, kManyPairs); }
+
+// The sum (add_pairs) of the values of the threads before this one; *total: of all.
 __device__ __forceinline__ int block_scan(int v, int *total, int *warp_sums) {
     const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31;
     int incl = v;
 #pragma unroll
     for (int o = 1; o < 32; o <<= 1) {
         const int y = __shfl_up_sync(kFull, incl, o);
-        if (lane >= o) incl += y;
+        if (lane >= o) incl = add_pairs(incl, y);
     }
+    const int excl = __shfl_up_sync(kFull, incl, 1);
     if (lane == 31) warp_sums[warp] = incl;
     __syncthreads();
     int w = warp_sums[lane];
 #pragma unroll
     for (int o = 1; o < 32; o <<= 1) {
         const int y = __shfl_up_sync(kFull, w, o);
-        if (lane >= o) w += y;
+        if (lane >= o) w = add_pairs(w, y);
     }
     *total = __shfl_sync(kFull, w, 31);
     const int off = __shfl_sync(kFull, w, warp > 0 ? warp - 1 : 0);
     __syncthreads();
-    return (warp > 0 ? off : 0) + incl - v;
+    return add_pairs(warp > 0 ? off : 0, lane > 0 ? excl : 0);
 }
 
 // Lists every sequence's row pairs in buckets of falling key count (a counting sort; the
@@ -189,16 +196,16 @@ __global__ void __launch_bounds__(kPlanThreads, 1) packed_plan_kernel(const Plan
         int pairs = 0;
         // rows outside the tensors or a sequence longer than announced: skipped and flagged
         if (a < 0 || b < a || b > p.num_tokens || b - a > p.max_len) bad = true;
-        else pairs = (b - a + p.pair_tokens - 1) / p.pair_tokens;
+        else if (b > a) pairs = (b - a - 1) / p.pair_tokens + 1;
         cum[s] = pairs;
-        sum += pairs;
+        sum = add_pairs(sum, pairs);
     }
     int total;
     int run = block_scan(sum, &total, warp_sums);
     for (int s = beg; s < end; ++s) {
         const int pairs = cum[s];
         cum[s] = run;
-        run += pairs;
+        run = add_pairs(run, pairs);
     }
     if (threadIdx.x == 0) cum[S] = total;
     // overlapping sequences could list more pairs than the list holds
@@ -794,7 +801,7 @@ size_t packed_workspace(int32_t num_tokens, int32_t num_seqs, int32_t g) {
 cudaError_t launch_prefill_packed(const PackedPrefill &a, cudaStream_t stream) {
     const int g = a.num_q_heads / a.num_kv_heads, d = a.head_dim;
     const int64_t jobs = max_jobs(a.num_tokens, a.num_seqs, g);
-    if (jobs * a.num_kv_heads > INT32_MAX / 2) return cudaErrorNotSupported;
+    if (jobs * a.num_kv_heads >= kManyPairs) return cudaErrorNotSupported;
     PlanParams pl;
     pl.starts = a.starts;
     pl.meta = static_cast<int32_t *>(a.workspace);

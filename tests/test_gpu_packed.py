@@ -181,6 +181,24 @@ def test_bad_starts_are_flagged(pa):
 
 
 @pytest.mark.gpu
+@pytest.mark.parametrize("tokens,seqs,hq", [(300, 40, 4), (32 * (2 ** 19 + 1), 16384, 8)])
+def test_starts_that_go_back_and_forth_list_nothing(pa, tokens, seqs, hq):
+    """Starts 0, T, 0, T, ...: every second sequence is all of the rows.  Their pairs do not fit
+    the list, also where 32-bit sums of them would come round to a small number (the second
+    case: 8192 x (2^19 + 1) = 2^32 + 8192): flagged, and no row is written."""
+    torch = torch_mod()
+    z = lambda h: torch.empty(tokens, h, 64, dtype=torch.bfloat16, device="cuda")
+    q, k, v, out = z(hq), z(1), z(1), z(hq).fill_(7)
+    starts = torch.zeros(seqs + 1, dtype=torch.int32, device="cuda")
+    starts[1::2] = tokens
+    err = torch.zeros(1, dtype=torch.int32, device="cuda")
+    ws = torch.empty(pa.pa_prefill_packed_workspace_size(tokens, seqs, hq, 1), dtype=torch.uint8, device="cuda")
+    pa.pa_prefill_packed(q, k, v, starts, tokens, 0.1, out, ws, err)
+    assert pa.pa_wait(err) == pa.PA_DEVERR_CHUNK
+    assert (out[::101] == 7).all() and (out[-300:] == 7).all()
+
+
+@pytest.mark.gpu
 def test_many_sequences_and_a_long_one(pa):
     rng = np.random.default_rng(12)
     starts = np.concatenate([[0], np.cumsum(rng.integers(0, 9, 3000))])
