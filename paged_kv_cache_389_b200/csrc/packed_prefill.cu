@@ -29,6 +29,11 @@
 // Tried and slower: output rows written by four more warps (128 registers a thread at launch:
 // 184 us against 170 for 16 x 1024 tokens) or after the next job's first tile (189); jobs
 // ordered by sequence instead of longest first (177).
+// Within a softmax step, all slower: exponentials with the old reference point while the new
+// maximum is found (16 sequences up to 2048: 213 us against 179); the next tile's first scores
+// fetched between them (203); P handed over in two halves (183); the two streams taking turns
+// at the exponentials (2 x 8192: 2,130 us against 2,035).  d = 64 with 64, 96, 112 keys a tile: 95,
+// 92, 90 us against 85.
 // A share of the exponentials on the FMA units (a cubic in the fraction) was tried at 1, 2
 // and 3 of 8: no gain at d = 128, 3 to 9 % slower at d = 64, so there is none.
 //
@@ -85,6 +90,11 @@ struct Tiles {
     static constexpr int kKeys = D == 128 ? 80 : 128;
     static constexpr uint32_t kP = kKeys, kO = 256 - D, kStream = 256, kCols = 512;
     static_assert(kP + kKeys / 2 <= kO, "S, P and O of a stream share 256 columns");
+    // Sixteens of keys whose exponentials are taken before P_t is known to be free (kept in the
+    // registers that their scores held): the last PV is waited for behind them.  In the order of
+    // 0, 1, 3, all: 2 x 8192 tokens 2,002, 1,961, 1,961, 1,971 us (at the power limit), 16
+    // sequences up to 2048 184, 179, 178, 179 us; d = 64: 85, 85, 85, 87 us.
+    static constexpr int kAhead = 3;
     static_assert(kKeys % 16 == 0, "whole k steps");
 };
 constexpr uint32_t kQHalf = kTile * 128;   // 64 columns of a 128-row tile in shared memory
@@ -621,47 +631,54 @@ __global__ void __launch_bounds__(kThreads, 1) packed_prefill_kernel(const __gri
                 const float m_new = fmaxf(m, fmaxf(fmax3(a0, a1, a2), a3) * sl2);
                 const bool move = j > 0 && row_ok && m_new > m + kRescaleLog2;
                 const bool any_move = __any_sync(kFull, move);
-                if (j == 0) m = m_new;
+                const float m_old = m;
+                if (j == 0 || move) m = m_new;
                 // P_t may be written, and O_t rescaled, once the stream's last PV is done
-                if (ns > 0) {
-                    live = wait_bar(&bars[kBarPFree + t], (ns - 1) & 1, abort_flag, p);
-                    live = __all_sync(kFull, live);
-                    if (!live) break;
-                    tc::fence_after();
-                }
-                ++ns;
-                if (any_move) {
-                    const float alpha = move ? fast_exp2(m - m_new) : 1.f;
-                    if (move) m = m_new;
+                auto own_p = [&]() {
+                    if (ns > 0) {
+                        live = wait_bar(&bars[kBarPFree + t], (ns - 1) & 1, abort_flag, p);
+                        live = __all_sync(kFull, live);
+                        if (!live) return;
+                        tc::fence_after();
+                    }
+                    ++ns;
+                    if (!any_move) return;
+                    const float alpha = move ? fast_exp2(m_old - m) : 1.f;
                     l *= alpha;
 #pragma unroll 1
                     for (int c = 0; c < D; c += 16) {
                         float ov[16];
                         tc::ld16(tO + c, ov);
                         tc::wait_ld();
-                        uint32_t w[16];
+                        uint32_t x[16];
 #pragma unroll
-                        for (int i = 0; i < 16; ++i) w[i] = __float_as_uint(ov[i] * alpha);
-                        tc::st16(tO + c, w);
+                        for (int i = 0; i < 16; ++i) x[i] = __float_as_uint(ov[i] * alpha);
+                        tc::st16(tO + c, x);
                     }
-                }
+                };
                 const float ref = m == -INFINITY ? 0.f : m;
                 const float2 sc2 = make_float2(sl2, sl2), nm2 = make_float2(-ref, -ref);
                 float2 acc0 = make_float2(0.f, 0.f), acc1 = acc0;
+                uint32_t w[kKeys / 16][8];
 #pragma unroll
-                for (int c = 0; c < kKeys; c += 16) {
-                    uint32_t w[8];
+                for (int c = 0; c < kKeys / 16; ++c) {
 #pragma unroll
                     for (int i = 0; i < 8; ++i) {
-                        float2 x = __ffma2_rn(make_float2(sv[c + 2 * i], sv[c + 2 * i + 1]), sc2, nm2);
+                        float2 x = __ffma2_rn(make_float2(sv[16 * c + 2 * i], sv[16 * c + 2 * i + 1]), sc2, nm2);
                         x.x = fast_exp2(x.x);
                         x.y = fast_exp2(x.y);
                         if (i & 1) acc1 = __fadd2_rn(acc1, x);
                         else acc0 = __fadd2_rn(acc0, x);
-                        w[i] = pack_bf16x2(x.x, x.y);
+                        w[c][i] = pack_bf16x2(x.x, x.y);
                     }
-                    tc::st8(tP + c / 2, w);
+                    if (c + 1 == TL::kAhead) {
+                        own_p();
+#pragma unroll
+                        for (int e = 0; e < c; ++e) tc::st8(tP + e * 8, w[e]);
+                    }
+                    if (c + 1 >= TL::kAhead) tc::st8(tP + c * 8, w[c]);
                 }
+                if (!live) break;
                 l += (acc0.x + acc0.y) + (acc1.x + acc1.y);
                 tc::wait_st();
                 tc::fence_before();
