@@ -282,7 +282,8 @@ def pa_prefill_chunk(query, key_cache, value_cache, block_tables, context_lens, 
 # raw handle 0.1).
 def _run(fn, name, dev, stream, *args):
     """Call the library's fn with the stream's handle appended, with device `dev` current."""
-    assert dev >= 0, "tensors passed to the library must be on a CUDA device"
+    if dev < 0:
+        raise AssertionError("tensors passed to the library must be on a CUDA device")
     cuda = _torch().cuda
     handle = _torch()._C._cuda_getCurrentRawStream(dev) if stream is None else stream.cuda_stream
     if dev == cuda.current_device():
@@ -402,7 +403,8 @@ def pa_decode_scaled_workspace_size(num_q_heads, num_kv_heads, head_dim) -> int:
 
 
 def _workspace(t, dev):
-    assert t.get_device() == dev and t.is_contiguous(), "workspace: contiguous and on the other tensors' device"
+    if t.get_device() != dev or not t.is_contiguous():
+        raise AssertionError("workspace: contiguous and on the other tensors' device")
     return t.data_ptr(), t.numel() * t.element_size()
 
 
@@ -414,7 +416,8 @@ def pa_decode_scaled(query, key_cache, value_cache, key_scales, value_scales, bl
     kc, vc, ks, vs, desc = _scaled_pool(key_cache, value_cache, key_scales, value_scales, dev)
     shape = query.shape
     S, hq, d = shape
-    assert d == key_cache.shape[3], "query: head_dim of the pools wanted"
+    if d != key_cache.shape[3]:
+        raise AssertionError("query: head_dim of the pools wanted")
     mb = block_tables.shape[-1]
     ws, ws_bytes = _workspace(workspace, dev)
     _run(_lib.pa_decode_scaled, "pa_decode_scaled", dev, stream, _p(query, torch.bfloat16, shape, dev, "query"), kc, vc, ks, vs,

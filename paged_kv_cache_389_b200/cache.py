@@ -9,6 +9,7 @@ cache write, then attention, all on one stream.
 """
 from __future__ import annotations
 
+import contextlib
 import math
 
 import numpy as np
@@ -75,26 +76,29 @@ class PagedKVCache:
         """Allocate slots for ``counts[i]`` new tokens of each seq (default 1), all or
         nothing, in one call to the host manager.  Returns (int64 slots [sum counts],
         int32 copy pairs [P, 2]) as numpy arrays."""
+        if self.block_scales and len(set(seqs)) != len(seqs):
+            raise ValueError("block_scales: a block's tokens stand next to each other in a step, so no sequence twice")
         return self.manager.append_step(seqs, counts)
 
     def write(self, k, v, slots, pairs=None, stream=None):
         """Copy-on-write copies (if any), then scatter k/v [T, Hkv, d] into ``slots``."""
         torch = _torch()
+        if self.block_scales:
+            with self._on(stream):
+                scales = self.key_scales, self.value_scales
+                if pairs is not None and len(pairs):
+                    pairs = torch.as_tensor(pairs, device=self.device)
+                    pa_copy_blocks_scaled(self.key_cache, self.value_cache, *scales, pairs, self.err_flag)
+                if len(slots):
+                    slots = torch.as_tensor(slots, device=self.device)
+                    pa_cache_write_scaled(k, v, slots, self.key_cache, self.value_cache, *scales, self.err_flag)
+            return
         if pairs is not None and len(pairs):
             pairs = torch.as_tensor(pairs, device=self.device)
-            if self.block_scales:
-                pa_copy_blocks_scaled(self.key_cache, self.value_cache, self.key_scales, self.value_scales, pairs,
-                                      self.err_flag, stream)
-            else:
-                pa_copy_blocks(self.key_cache, self.value_cache, pairs, self.err_flag, stream)
+            pa_copy_blocks(self.key_cache, self.value_cache, pairs, self.err_flag, stream)
         if len(slots):
             slots = torch.as_tensor(slots, device=self.device)
-            if self.block_scales:
-                pa_cache_write_scaled(k, v, slots, self.key_cache, self.value_cache, self.key_scales, self.value_scales,
-                                      self.err_flag, stream)
-            else:
-                pa_cache_write(k, v, slots, self.key_cache, self.value_cache, self.err_flag, stream, self.k_scale,
-                               self.v_scale)
+            pa_cache_write(k, v, slots, self.key_cache, self.value_cache, self.err_flag, stream, self.k_scale, self.v_scale)
 
     def append(self, seqs, k, v, counts=None, stream=None):
         slots, pairs = self.plan_append(seqs, counts)
@@ -112,15 +116,18 @@ class PagedKVCache:
     def decode(self, q, seqs, scale, out=None, partition_size=0, max_blocks=None, stream=None,
                workspace=None):
         torch = _torch()
+        if self.block_scales:    # the context is always split: partition_size says nothing here
+            with self._on(stream):
+                tables, lens, max_len = self.tables(seqs, max_blocks)
+                out = torch.empty_like(q) if out is None else out
+                if workspace is None:
+                    workspace = self._scratch(pa_decode_scaled_workspace_size(q.shape[1], self.num_kv_heads, q.shape[2]))
+                pa_decode_scaled(q, self.key_cache, self.value_cache, self.key_scales, self.value_scales, tables, lens,
+                                 max(max_len, 1), scale, out, workspace, self.err_flag)
+            return out
         tables, lens, max_len = self.tables(seqs, max_blocks)
         max_len = max(max_len, 1)
         out = torch.empty_like(q) if out is None else out
-        if self.block_scales:    # the context is always split: partition_size says nothing here
-            if workspace is None:
-                workspace = self._scratch(pa_decode_scaled_workspace_size(q.shape[1], self.num_kv_heads, q.shape[2]), stream)
-            pa_decode_scaled(q, self.key_cache, self.value_cache, self.key_scales, self.value_scales, tables, lens, max_len,
-                             scale, out, workspace, self.err_flag, stream)
-            return out
         if partition_size and workspace is None:
             ws = pa_decode_workspace_size(len(seqs), q.shape[1], q.shape[2], max_len, partition_size)
             workspace = torch.empty(max(ws, 16), dtype=torch.uint8, device=self.device)
@@ -128,13 +135,14 @@ class PagedKVCache:
                   partition_size, workspace, self.err_flag, stream, self.k_scale, self.v_scale)
         return out
 
-    def _scratch(self, nbytes, stream):
-        """Workspace for one call on `stream` (None: the current one)."""
+    def _on(self, stream):
+        """Makes `stream` (None: leaves it alone) the current one, so that a call's tables, slots
+        and scratch are made, copied and given back in its order."""
+        return contextlib.nullcontext() if stream is None else _torch().cuda.stream(stream)
+
+    def _scratch(self, nbytes):
         torch = _torch()
-        ws = torch.empty(max(nbytes, 16), dtype=torch.uint8, device=self.device)
-        if stream is not None:
-            ws.record_stream(stream)
-        return ws
+        return torch.empty(max(nbytes, 16), dtype=torch.uint8, device=self.device)
 
     def prompt(self, q, k, v, seqs, counts, scale, out=None, stream=None):
         """Whole prompts of empty sequences: causal attention over each of them and their
@@ -142,22 +150,29 @@ class PagedKVCache:
         of seqs[i] after those of seqs[i - 1] (their tokens may be strided).  Returns the
         attention's output [T, Hq, d]."""
         torch = _torch()
-        counts = [int(c) for c in counts]
-        if any(self.manager.num_tokens(s) != 0 for s in seqs):
-            raise ValueError("prompt() takes sequences without tokens; prefill() continues others")
-        if sum(counts) != q.shape[0]:
-            raise ValueError("counts must add up to the rows of q")
-        slots, pairs = self.plan_append(seqs, counts)
-        starts = torch.zeros(len(counts) + 1, dtype=torch.int32)
-        starts[1:] = torch.cumsum(torch.tensor(counts, dtype=torch.int64), 0)
-        out = torch.empty(q.shape, dtype=q.dtype, device=self.device) if out is None else out
-        ws = self._scratch(pa_prefill_packed_workspace_size(q.shape[0], len(counts), q.shape[1], self.num_kv_heads), stream)
-        pa_prefill_packed(q, k, v, starts.to(self.device), max(counts, default=0), scale, out, ws, self.err_flag, stream)
-        self.write(k if self.block_scales else k.contiguous(), v if self.block_scales else v.contiguous(), slots, pairs, stream)
+        seqs, counts = list(seqs), [int(c) for c in counts]
+        if len(set(seqs)) != len(seqs) or any(self.manager.num_tokens(s) != 0 for s in seqs):
+            raise ValueError("prompt() takes different sequences without tokens; prefill() continues others")
+        if len(counts) != len(seqs) or min(counts, default=0) < 0 or sum(counts) != q.shape[0]:
+            raise ValueError("counts: one per sequence, adding up to the rows of q")
+        if self.dtype == torch.float32:
+            raise ValueError("prompt() computes in bf16: a bf16 or 8-bit pool wanted")
+        with self._on(stream):
+            starts = torch.from_numpy(np.concatenate([[0], np.cumsum(counts)]).astype(np.int32)).to(self.device)
+            out = torch.empty(q.shape, dtype=q.dtype, device=self.device) if out is None else out
+            ws = self._scratch(pa_prefill_packed_workspace_size(q.shape[0], len(counts), q.shape[1], self.num_kv_heads))
+            # what this refuses, it refuses before the manager hands out blocks
+            pa_prefill_packed(q, k, v, starts, max(counts, default=0), scale, out, ws, self.err_flag)
+            slots, pairs = self.plan_append(seqs, counts)
+            if not self.block_scales:
+                k, v = k.contiguous(), v.contiguous()
+            self.write(k, v, slots, pairs)
         return out
 
     def prefill(self, q, seqs, chunk_lens, scale, out=None, max_blocks=None, stream=None):
         torch = _torch()
+        if self.block_scales:
+            raise ValueError("prefill() reads bf16 pools; prompt() fills one with a scale per block and kv head")
         tables, lens, _ = self.tables(seqs, max_blocks)
         out = torch.empty_like(q) if out is None else out
         ch = torch.as_tensor(np.asarray(chunk_lens, np.int32), device=self.device)

@@ -12,7 +12,8 @@
 // only when a p or a w passes 2^8 (a vote per block), so the reductions over lanes
 // are rare.  Sums, maxima and O are fp32; p, w are rounded to f16 (relative 2^-11) for
 // the product with V; codes are exact in f16; the query is scaled per head by a power
-// of two into the middle of f16's range, which keeps every bf16 bit of it.
+// of two into the middle of f16's range, which keeps every bf16 bit of its elements down
+// to 2^-24 of the head's largest (smaller ones are off by at most 2^-32 of it).
 //
 // What bounds it: HBM, 2 * L * Hkv * d bytes.  So:
 //  * Work is cut evenly whatever the lengths are: the blocks of all (sequence, kv head)
@@ -91,7 +92,7 @@ __device__ __forceinline__ int checked_len(const Params &p, int s) {
     const int L = __ldg(p.lens + s);
     return L < 0 || L > p.max_context || (int64_t)L > (int64_t)p.max_blocks * kBlockSize ? -1 : L;
 }
-__device__ __forceinline__ int blocks_of(int tokens) { return tokens > 0 ? (tokens + kBlockSize - 1) / kBlockSize : 0; }
+__device__ __forceinline__ int blocks_of(int tokens) { return tokens > 0 ? (tokens - 1) / kBlockSize + 1 : 0; }
 
 // Four codes -> two f16x2 (bytes 0, 1 and bytes 2, 3).
 template <bool kInt8>

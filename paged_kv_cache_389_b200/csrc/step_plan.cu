@@ -107,7 +107,7 @@ __global__ void __launch_bounds__(kPlanThreads, 1) step_plan_kernel(const StepPl
         if constexpr (kRelease) {
             nb = !wrong && cnt != 0 ? (uint32_t)blocks_of(len) : 0u;
         } else {
-            wrong = wrong || cnt < 0 || (int64_t)len + cnt > (int64_t)p.max_blocks * kBlockSize;
+            wrong = wrong || cnt < 0 || (int64_t)len + cnt > min((int64_t)p.max_blocks * kBlockSize, (int64_t)INT32_MAX);
             if (!wrong) {
                 na = min((uint32_t)cnt, kSat);
                 nb = min((uint32_t)(blocks_of(len + cnt) - blocks_of(len)), kSat);

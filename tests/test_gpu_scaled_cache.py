@@ -463,3 +463,32 @@ def test_decode_in_graphs_that_share_a_workspace(pa, code):
     a.call(stream=side)
     side.synchronize()
     a.check()
+
+
+@pytest.mark.gpu
+def test_a_context_of_2_31_tokens(pa):
+    """One context of 2^31 - 1 tokens (every table entry names the same block): the line of items,
+    the lengths and the last block's tail hold at the end of 32 bits."""
+    torch = torch_mod()
+    rng = np.random.default_rng(31)
+    L, d, n = 2 ** 31 - 1, 64, 2 ** 27
+    kc = torch.from_numpy(rng.integers(-127, 128, (1, 1, 16, d)).astype(np.int8)).cuda()
+    vc = torch.from_numpy(rng.integers(-127, 128, (1, 1, 16, d)).astype(np.int8)).cuda()
+    ks, vs = torch.full((1, 1), 2.0 ** -7, device="cuda"), torch.full((1, 1), 2.0 ** -6, device="cuda")
+    q = torch.from_numpy(rng.standard_normal((1, 2, d)).astype(np.float32)).to(torch.bfloat16).cuda()
+    tables = torch.zeros(1, n, dtype=torch.int32, device="cuda")
+    lens, err = torch.tensor([L], dtype=torch.int32, device="cuda"), torch.zeros(1, dtype=torch.int32, device="cuda")
+    out = torch.empty_like(q)
+    ws = torch.empty(pa.pa_decode_scaled_workspace_size(2, 1, d), dtype=torch.uint8, device="cuda")
+    pa.pa_decode_scaled(q, kc, vc, ks, vs, tables, lens, L, 0.125, out, ws, err)
+    assert pa.pa_wait(err) == 0
+    k, v = kc.double().cpu().numpy()[0, 0] * 2.0 ** -7, vc.double().cpu().numpy()[0, 0] * 2.0 ** -6
+    s = 0.125 * q.double().cpu().numpy()[0] @ k.T
+    w = np.exp(s - s.max(1, keepdims=True)) * np.where(np.arange(16) < 15, n, n - 1)
+    w /= w.sum(1, keepdims=True)
+    # a warp of at least 148 x 12 adds n / 1776 blocks to its sums one after the other, each addition
+    # off by 2^-24 of the sum: in the sum of the weights and in the weighted one; then the roundings
+    # of the weights (f16) and the output (bf16), 2^-10 for the exponentials and scores
+    tol = 2 * (n / 1776) * 2.0 ** -24 + 2.0 ** -11 + 2.0 ** -8 + 2.0 ** -10
+    far = np.abs(out.double().cpu().numpy()[0] - w @ v) - tol * (w @ np.abs(v))
+    assert (far <= 0).all()

@@ -95,6 +95,10 @@ def test_paged_cache_with_block_scales(pa, code):
     within(f64(out), o, mass, reach, (0, 2.0 ** -8, 0.0))
     with pytest.raises(ValueError):
         kv.prompt(q, k, v, [0, 1], counts, scale)
+    with pytest.raises(ValueError):
+        kv.append([0, 1, 0], k[:3], v[:3])
+    with pytest.raises(ValueError):
+        kv.prefill(q[:2].unsqueeze(1), [0, 1], [1, 1], scale)
     kv.fork(0, 2)
     for _ in range(3):
         kn, vn, qn = rows(rng, 3, hkv, d), rows(rng, 3, hkv, d), rows(rng, 3, hq, d)
@@ -135,3 +139,53 @@ def test_prompt_on_a_bf16_cache(pa):
     within(f64(out), o, mass, reach, (0, 2.0 ** -8, 0.0))
     within(np.concatenate([f64(chunk[0]), f64(chunk[1, :50])]), o, mass, reach, (0, 2.0 ** -8, 0.0))
     assert pa.pa_wait(kv.err_flag) == 0
+
+
+def test_prompt_refusals_leave_the_manager_alone(pa):
+    from paged_kv_cache_389_b200.cache import PagedKVCache
+    torch = torch_mod()
+    rng = np.random.default_rng(1)
+    kv = PagedKVCache(8, 2, 64, torch.int8, block_scales=True)
+    for s in (0, 1):
+        kv.add_seq(s)
+    q, k, v = rows(rng, 40, 8, 64).split([4, 2, 2], 1)
+    for seqs, counts in (([0, 0], [20, 20]), ([0, 1], [20, 21]), ([0, 1], [40]), ([0, 1], [50, -10])):
+        with pytest.raises(ValueError):
+            kv.prompt(q, k, v, seqs, counts, 0.1)
+    with pytest.raises(pa.PAError):    # six query heads on two kv heads: no group of three
+        kv.prompt(rows(rng, 40, 6, 64), k, v, [0, 1], [20, 20], 0.1)
+    big = rows(rng, 200, 8, 64)
+    with pytest.raises(pa.PAError):    # 13 blocks of a pool of 8
+        kv.prompt(*big.split([4, 2, 2], 1), [0, 1], [100, 100], 0.1)
+    assert kv.manager.num_tokens(0) == 0 and kv.manager.num_tokens(1) == 0 and kv.manager.num_free() == 8
+    with pytest.raises(ValueError):
+        PagedKVCache(8, 2, 64, torch.float32).prompt(q, k, v, [], [], 0.1)
+    kv.prompt(q[:0], k[:0], v[:0], [0, 1], [0, 0], 0.1)
+    assert pa.pa_wait(kv.err_flag) == 0
+
+
+def test_calls_on_a_stream_of_their_own(pa):
+    """Prompts, appends and decodes through PagedKVCache on a side stream while the current one
+    allocates and overwrites: nothing a call made for itself is taken from under it."""
+    from paged_kv_cache_389_b200.cache import PagedKVCache
+    torch = torch_mod()
+    rng = np.random.default_rng(8)
+    fused, qn = rows(rng, 500, 8, 64), rows(rng, 2, 4, 64)
+    q, k, v = fused.split([4, 2, 2], 1)
+    results = []
+    for side in (None, torch.cuda.Stream()):
+        kv = PagedKVCache(64, 2, 64, torch.float8_e4m3fn, block_scales=True)
+        kv.add_seq(0)
+        kv.add_seq(1)
+        torch.cuda.synchronize()
+        outs = [kv.prompt(q, k, v, [0, 1], [300, 200], 0.1, stream=side)]
+        for i in range(8):
+            kv.append([0, 1], k[i:i + 2], v[i:i + 2], stream=side)
+            outs.append(kv.decode(qn, [0, 1], 0.1, stream=side))
+            for n in (4, 8, 64, 4096, 1 << 20):    # the sizes of the calls' own tensors
+                torch.full((n,), 0x7FFFFFFF, dtype=torch.int32, device="cuda")
+        torch.cuda.synchronize()
+        assert int(kv.err_flag) == 0
+        results.append(outs)
+    for a, b in zip(*results):
+        assert torch.equal(a, b)

@@ -128,6 +128,22 @@ def test_a_step_that_does_not_fit_changes_nothing(pa, fault, big):
 
 
 @pytest.mark.gpu
+def test_lengths_next_to_2_31(pa):
+    """A table row of more than 2^31 tokens: lengths stop at what 32 bits hold."""
+    torch = torch_mod()
+    mb = 2 ** 27 + 8
+    tables = torch.full((1, mb), 5, dtype=torch.int32, device="cuda")
+    one = lambda *x, dt=torch.int32: torch.tensor(x, dtype=dt, device="cuda")
+    for held, count, good in ((2 ** 31 - 1, 16, False), (2 ** 31 - 4, 4, False), (2 ** 31 - 4, 3, True)):
+        lens, nf, err, slots, starts = one(held), one(3), one(0), one(*([7] * 5), dt=torch.int64), one(0, 0)
+        pa.pa_step_plan(one(count), lens, tables, one(1, 2, 3), nf, slots, starts, err_flag=err)
+        assert pa.pa_wait(err) == (0 if good else pa.PA_DEVERR_PLAN)
+        assert int(lens) == (held + count if good else held) and int(nf) == 3
+        assert slots.tolist() == ([92, 93, 94, -1, -1] if good else [-1] * 5)
+        assert starts.tolist() == ([0, count] if good else [0, 0])
+
+
+@pytest.mark.gpu
 def test_a_negative_table_entry_is_flagged(pa):
     counts, lens = np.array([2, 1], np.int32), np.array([5, 16], np.int32)
     tables = np.array([[-1, -1], [4, -1]], np.int32)
