@@ -33,6 +33,9 @@
  * saturated to +-448, value = e4m3 * scale.  key/value inputs, query and out are
  * then bf16.  pa_cache_write, pa_copy_blocks, pa_decode and pa_append_decode take
  * it with head_dim 128; pa_prefill_chunk returns PA_ERR_UNSUPPORTED.
+ * 8-bit KV cache with a scale per (block, kv head): pa_cache_write_scaled,
+ * pa_copy_blocks_scaled and pa_decode_scaled take pools of PA_FP8_E4M3 or PA_INT8
+ * codes beside float scale arrays; the other calls refuse PA_INT8.
  *
  * Conventions:
  *   - Ownership: the caller owns every buffer, the decode workspace included.
@@ -55,7 +58,8 @@
  *     capture time.  Cache writes, block copies, unsplit decodes, split decodes of
  *     fp32 or fp8 pools or head_dim 64, and prefills with more than 8 jobs per
  *     SM (jobs = num_seqs * num_kv_heads * ceil(max_chunk * g / 256)) replay
- *     correctly.  Issue directly, not from a graph: a split decode (pa_decode,
+ *     correctly, and so do pa_step_plan, pa_step_release, pa_prefill_packed and the
+ *     calls for pools with block scales.  Issue directly, not from a graph: a split decode (pa_decode,
  *     pa_append_decode, pa_decode_static_scratch) of bf16 pools with head_dim 128,
  *     whose shared-prefix detection tags its flags with a per-call value (a replay
  *     would read the previous replay's table comparison), and a pa_prefill_chunk

@@ -80,13 +80,16 @@ template <bool kInt8, bool kFinite>
 __device__ __forceinline__ uint32_t encode_bf16x4(uint32_t w0, uint32_t w1, float inv) {
     const float2 a = __bfloat1622float2(*reinterpret_cast<const __nv_bfloat162 *>(&w0));
     const float2 b = __bfloat1622float2(*reinterpret_cast<const __nv_bfloat162 *>(&w1));
+    const float2 i2 = make_float2(inv, inv);
     if constexpr (kInt8 && kFinite) {
-        constexpr float kMagic = 12582912.f;
-        const uint32_t lo = __byte_perm(__float_as_uint(fmaf(a.x, inv, kMagic)), __float_as_uint(fmaf(a.y, inv, kMagic)), 0x0040);
-        const uint32_t hi = __byte_perm(__float_as_uint(fmaf(b.x, inv, kMagic)), __float_as_uint(fmaf(b.y, inv, kMagic)), 0x0040);
+        const float2 magic = make_float2(12582912.f, 12582912.f);
+        const float2 x = __ffma2_rn(a, i2, magic), y = __ffma2_rn(b, i2, magic);
+        const uint32_t lo = __byte_perm(__float_as_uint(x.x), __float_as_uint(x.y), 0x0040);
+        const uint32_t hi = __byte_perm(__float_as_uint(y.x), __float_as_uint(y.y), 0x0040);
         return __byte_perm(lo, hi, 0x5410);
     }
-    return encode4<kInt8>(a.x * inv, a.y * inv, b.x * inv, b.y * inv);
+    const float2 x = __fmul2_rn(a, i2), y = __fmul2_rn(b, i2);
+    return encode4<kInt8>(x.x, x.y, y.x, y.y);
 }
 
 // Four codes re-expressed under a larger scale: round(code * ratio).
@@ -109,9 +112,12 @@ __device__ __forceinline__ uint32_t recode4(uint32_t w, float ratio) {
 
 // D: head_dim.  A warp covers kRows rows of D elements per load, 16 bytes a lane.
 // window: tokens whose runs one warp looks after.
-// Eight CTAs to an SM: 32 warps, each with 4 KB of rows in flight, at 64 registers (the few
-// that spill belong to the rare paths).  102 MB of prompts: 21.3 us, 4.8 TB/s; with 4, 5, 6, 7
-// CTAs 26.8, 23.5, 22.7, 21.8, with 9 or 10 (rows spill) 24.7, 40.8.  256 tokens: 4.8 us.
+// Eight CTAs to an SM: 32 warps, each with 4 KB of rows in flight, at 64 registers (what
+// spills belongs to the rare paths).  102 MB of prompts: 19.0 us, 5.4 TB/s (floor 15.5); with 7
+// CTAs 19.6, with 9 (rows spill) 21.7.  256 tokens: 3.95 us, the latency of one warp's chain of
+// loads.  The instructions count as much as the bytes (issue slots 71 % taken with a path for
+// every order of slots: 21.3 and 4.8 us), so runs of ascending slots have one of their own, and
+// earlier tokens are re-expressed last, when the rows' registers are free (19.4 before).
 template <int D, bool kInt8>
 __global__ void __launch_bounds__(kWriteWarps * 32, kWriteCtas) cache_write_scaled_kernel(const __grid_constant__ ScaledWrite p,
                                                                               int window) {
@@ -175,82 +181,114 @@ __global__ void __launch_bounds__(kWriteWarps * 32, kWriteCtas) cache_write_scal
             n += k;
             more = k == 32;
         }
-        // pass 1: the rows, 16 at a time (the last 16 stay in registers), and their maximum
-        uint4 row[kPasses];
-        uint32_t am = 0;
-        auto load = [&](int first) {
-#pragma unroll
-            for (int k = 0; k < kPasses; ++k) {
-                const int t = first + k * kRows + r0;
-                row[k] = make_uint4(0, 0, 0, 0);
-                if (t < n) row[k] = __ldg(reinterpret_cast<const uint4 *>(base + (int64_t)(i0 + t) * stride));
-            }
-        };
-        for (int first = 0; first < n; first += kBlockSize) {
-            load(first);
-#pragma unroll
-            for (int k = 0; k < kPasses; ++k) am = amax2(amax2(amax2(amax2(am, row[k].x), row[k].y), row[k].z), row[k].w);
-        }
-        uint32_t a16 = __reduce_max_sync(kFull, max(am & 0xffffu, am >> 16));
-        const bool finite = a16 < kInfBits;
-        if (!finite) {   // once more without the infinities and NaN
-            am = 0;
-            for (int first = 0; first < n; first += kBlockSize) {
-                if (n > kBlockSize) load(first);
-#pragma unroll
-                for (int k = 0; k < kPasses; ++k)
-                    am = amax2_finite(amax2_finite(amax2_finite(amax2_finite(am, row[k].x), row[k].y), row[k].z), row[k].w);
-            }
-            a16 = __reduce_max_sync(kFull, max(am & 0xffffu, am >> 16));
-        }
-        const int e_new = scale_exp<kInt8>(a16);
-        const bool fresh = (written & 1u) != 0u;
-        // a stored scale that is no finite positive number counts as none
-        const bool has_old = !fresh && old_scale > 0.f && old_scale < INFINITY;
-        float sigma = exp2_int(e_new);
-        if (has_old && old_scale > sigma) sigma = old_scale;
         unsigned char *block = pool + bh * (kBlockSize * D) + c * 8;
-        // earlier tokens of the block under the larger scale
-        if (has_old && sigma > old_scale) {
-            const float ratio = old_scale / sigma;
-            const uint32_t below = (2u << (31 - __clz(written))) - 1u;
-            const uint32_t keep = below & ~written;
-            uint2 held[kPasses];
-#pragma unroll
-            for (int k = 0; k < kPasses; ++k) {
-                const int o = k * kRows + r0;
-                if (keep >> o & 1u) held[k] = *reinterpret_cast<const uint2 *>(block + o * D);
-            }
-#pragma unroll
-            for (int k = 0; k < kPasses; ++k) {
-                const int o = k * kRows + r0;
-                if (keep >> o & 1u)
-                    *reinterpret_cast<uint2 *>(block + o * D) =
-                        make_uint2(recode4<kInt8>(held[k].x, ratio), recode4<kInt8>(held[k].y, ratio));
-            }
-        }
-        if (lane == 0 && !(has_old && sigma == old_scale)) scales[bh] = sigma;
-        // pass 2: the codes (rows of runs beyond 16 tokens are loaded again)
-        const float inv = 1.f / sigma;
-        auto store = [&](auto all_finite) {
-            constexpr bool kFin = decltype(all_finite)::value;
-            for (int f = 0; f < n; f += kBlockSize) {
-                if (n > kBlockSize) load(f);
+        // |x| bits of a row's piece into the running maximum
+        auto maximum = [&](uint32_t m, const uint4 &x) { return amax2(amax2(amax2(amax2(m, x.x), x.y), x.z), x.w); };
+        auto maximum_finite = [&](uint32_t m, const uint4 &x) {
+            return amax2_finite(amax2_finite(amax2_finite(amax2_finite(m, x.x), x.y), x.z), x.w);
+        };
+        auto over_warp = [&](uint32_t m) { return __reduce_max_sync(kFull, max(m & 0xffffu, m >> 16)); };
+        // The scale for a run of maximum a16 that writes the slots of `written`, stored.
+        bool grown = false;
+        auto settle = [&](uint32_t a16, uint32_t written) -> float {
+            // a stored scale that is no finite positive number counts as none
+            const bool has_old = (written & 1u) == 0u && old_scale > 0.f && old_scale < INFINITY;
+            float sigma = exp2_int(scale_exp<kInt8>(a16));
+            if (has_old && old_scale > sigma) sigma = old_scale;
+            if (lane == 0 && !(has_old && sigma == old_scale)) scales[bh] = sigma;
+            grown = has_old && sigma > old_scale;
+            return sigma;
+        };
+        // Earlier tokens of the block under a scale that has grown.
+        auto regrow = [&](float sigma, uint32_t written) {
+            if (grown) {
+                const float ratio = old_scale / sigma;
+                const uint32_t below = (2u << (31 - __clz(written))) - 1u;
+                const uint32_t keep = below & ~written;
+                uint2 held[kPasses];
 #pragma unroll
                 for (int k = 0; k < kPasses; ++k) {
-                    const int t = f + k * kRows + r0;
-                    // the token's offset in the block: held by lane l + t unless the run is a long one
-                    int o = __shfl_sync(kFull, off, (l + t) & 31);
-                    if (n > kBlockSize && t < n) o = (int)(p.slots[i0 + t] % kBlockSize);
-                    if (t < n)
+                    const int o = k * kRows + r0;
+                    if (keep >> o & 1u) held[k] = *reinterpret_cast<const uint2 *>(block + o * D);
+                }
+#pragma unroll
+                for (int k = 0; k < kPasses; ++k) {
+                    const int o = k * kRows + r0;
+                    if (keep >> o & 1u)
                         *reinterpret_cast<uint2 *>(block + o * D) =
-                            make_uint2(encode_bf16x4<kInt8, kFin>(row[k].x, row[k].y, inv),
-                                       encode_bf16x4<kInt8, kFin>(row[k].z, row[k].w, inv));
+                            make_uint2(recode4<kInt8>(held[k].x, ratio), recode4<kInt8>(held[k].y, ratio));
                 }
             }
         };
-        if (finite) store(std::true_type{});
-        else store(std::false_type{});
+        auto codes = [&](auto all_finite, const uint4 &x, float inv) {
+            constexpr bool kFin = decltype(all_finite)::value;
+            return make_uint2(encode_bf16x4<kInt8, kFin>(x.x, x.y, inv), encode_bf16x4<kInt8, kFin>(x.z, x.w, inv));
+        };
+        uint4 row[kPasses];
+        const int o0 = __shfl_sync(kFull, off, l);
+        const bool in_order = __all_sync(kFull, lane < l || lane >= l + n || off == o0 + (lane - l));
+        if (in_order && n <= kBlockSize) {
+            // ascending slots, as appends produce them: the rows stay in registers
+            const int64_t row_bytes = kRows * stride;
+            const unsigned char *at = base + (int64_t)(i0 + r0) * stride;
+            uint32_t am = 0;
+#pragma unroll
+            for (int k = 0; k < kPasses; ++k) {
+                row[k] = make_uint4(0, 0, 0, 0);
+                if (k * kRows + r0 < n) row[k] = __ldg(reinterpret_cast<const uint4 *>(at + k * row_bytes));
+            }
+#pragma unroll
+            for (int k = 0; k < kPasses; ++k) am = maximum(am, row[k]);
+            uint32_t a16 = over_warp(am);
+            const bool finite = a16 < kInfBits;
+            if (!finite) {   // once more without the infinities and NaN
+                am = 0;
+#pragma unroll
+                for (int k = 0; k < kPasses; ++k) am = maximum_finite(am, row[k]);
+                a16 = over_warp(am);
+            }
+            const uint32_t wr = ((1u << n) - 1u) << o0;
+            const float sigma = settle(a16, wr), inv = 1.f / sigma;
+            unsigned char *dst = block + (o0 + r0) * D;
+            auto store = [&](auto fin) {
+#pragma unroll
+                for (int k = 0; k < kPasses; ++k)
+                    if (k * kRows + r0 < n) *reinterpret_cast<uint2 *>(dst + k * kRows * D) = codes(fin, row[k], inv);
+            };
+            if (finite) store(std::true_type{});
+            else store(std::false_type{});
+            regrow(sigma, wr);
+        } else {
+            // any order, and slots named more than once: 16 rows at a time, fetched for each pass
+            uint32_t am = 0;
+            auto load = [&](int first) {
+#pragma unroll
+                for (int k = 0; k < kPasses; ++k) {
+                    const int t = first + k * kRows + r0;
+                    row[k] = make_uint4(0, 0, 0, 0);
+                    if (t < n) row[k] = __ldg(reinterpret_cast<const uint4 *>(base + (int64_t)(i0 + t) * stride));
+                }
+            };
+#pragma unroll 1
+            for (int first = 0; first < n; first += kBlockSize) {
+                load(first);
+#pragma unroll
+                for (int k = 0; k < kPasses; ++k) am = maximum_finite(am, row[k]);
+            }
+            const float sigma = settle(over_warp(am), written), inv = 1.f / sigma;
+            regrow(sigma, written);
+#pragma unroll 1
+            for (int first = 0; first < n; first += kBlockSize) {
+                load(first);
+#pragma unroll
+                for (int k = 0; k < kPasses; ++k) {
+                    const int t = first + k * kRows + r0;
+                    if (t < n)
+                        *reinterpret_cast<uint2 *>(block + (int)(p.slots[i0 + t] % kBlockSize) * D) =
+                            codes(std::false_type{}, row[k], inv);
+                }
+            }
+        }
         __syncwarp();
     }
 }

@@ -31,6 +31,11 @@
 //    are done, and only parts at the ends of a CTA's items go through the workspace (two
 //    per CTA, whatever the context) to a second kernel.  Where all contexts are short, CTAs
 //    take whole segments and there is no second kernel.
+//  * What is left (figures of the 1.08 GB case): the median warp is done after 159 us, at
+//    6.9 TB/s, the last after 183: the same 28 SMs in every run get 8 % less of the memory than
+//    the others, and an even cut waits for them.  Drawing the last eighth of the line in units from a
+//    counter brought the ends together (163 to 178 us) but cost more, in moving between units, in the
+//    counter's zeroing and in joining the units' parts: 195 us against 190.
 //  * QK^T as S^T = K Q^T and PV as O^T = V^T W^T on m16n8k16 f16 tiles with the
 //    block's 16 tokens (or 16 head dims) in M and the g heads in N: each thread reads
 //    whole 16-byte pieces of the code rows and widens them in registers.
@@ -470,7 +475,7 @@ __global__ void __launch_bounds__(kThreads, 1) decode_scaled_kernel(const __grid
     const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31;
     const int S = p.num_seqs, hkv = p.num_kv_heads, step = p.cum_step;
     const int ncum = (S + step - 1) / step;
-    grid_dep_launch();  // the join may be set up; it waits for this grid
+    if (!p.whole) grid_dep_launch();  // the join may be set up; it waits for this grid
     // prefix sums of blocks + 1, one chunk of entries per thread
     {
         const int per = (ncum + kThreads - 1) / kThreads;
