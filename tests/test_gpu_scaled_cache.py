@@ -171,6 +171,30 @@ def test_append_many_tokens_per_warp(pa, code):
 
 @pytest.mark.gpu
 @pytest.mark.parametrize("code", CODES)
+@pytest.mark.parametrize("H,d", [(2, 128), (8, 64)])
+@pytest.mark.parametrize("big", [False, True])
+@pytest.mark.parametrize("order", ["ascending", "twice"])
+def test_append_runs_of_a_block(pa, code, H, d, big, order):
+    """Runs in ascending order (of every length and first slot), and runs that name slots up to
+    three times (with the same row each time, so that it does not matter which one lands), in
+    calls where a warp looks after one token and after 16."""
+    rng = np.random.default_rng(17)
+    nb = 16000 // H if big else 140
+    runs = []
+    for b in rng.permutation(nb):
+        first = int(rng.integers(0, 16))
+        run = b * 16 + np.arange(first, int(rng.integers(first + 1, 17)))
+        runs.append(run if order == "ascending" else rng.permutation(np.repeat(run, rng.integers(1, 4, len(run)))))
+    slots = np.concatenate(runs).astype(np.int64)
+    assert (len(slots) * H * 2 > 32768) == big
+    kp, ks = random_pool(rng, nb, H, d, code)
+    rows = rng.standard_normal((nb * 16, H, d)) * np.exp(2 * rng.standard_normal((nb * 16, 1, 1)))
+    _, flag = check_write(pa, bf16(rows[slots]), bf16(-rows[slots]), slots, kp, kp, ks, ks, code)
+    assert flag == 0
+
+
+@pytest.mark.gpu
+@pytest.mark.parametrize("code", CODES)
 def test_append_edge_values(pa, code):
     """Zeros, infinities, NaN, subnormal and huge numbers, exact ties and exact maxima,
     stored scales that are no scale, padding and slots outside the pool."""
