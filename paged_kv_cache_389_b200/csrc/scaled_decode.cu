@@ -15,7 +15,9 @@
 // of two into the middle of f16's range, which keeps every bf16 bit of its elements down
 // to 2^-24 of the head's largest (smaller ones are off by at most 2^-32 of it).
 //
-// What bounds it: HBM, 2 * L * Hkv * d bytes.  So:
+// What bounds it: HBM, 2 * L * Hkv * d bytes (in a graph: 256 lognormal contexts, 32/8 heads, e4m3, 1.08
+// GB: 190 us, 5.7 TB/s; 64 contexts, 32/32 heads, int8, 0.58 GB: 102 us; 8 x 32768 tokens, 64/8
+// heads, 0.54 GB: 100 us).  So:
 //  * Work is cut evenly whatever the lengths are: the blocks of all (sequence, kv head)
 //    segments form one line (each segment followed by one empty item that stands for
 //    its fixed cost), and warp w of the grid takes items [w n, (w + 1) n).  No unit is
