@@ -3,8 +3,9 @@
 Orchestration only: the host C++ BlockManager decides slots, tables and copy
 pairs; pa_copy_blocks / pa_cache_write / pa_decode / pa_prefill_chunk (for a pool
 with a scale per block and kv head pa_copy_blocks_scaled / pa_cache_write_scaled /
-pa_decode_scaled) and pa_prefill_packed do all the device work.  Order within a step follows the pages' data flow (a new token is
-written back into the cache, then attended to): copy-on-write copies, then the
+pa_decode_scaled) and pa_prefill_packed do all the device work.  Order within a
+step follows the pages' data flow (a new token is written back into the cache,
+then attended to): copy-on-write copies, then the
 cache write, then attention, all on one stream.
 """
 from __future__ import annotations
