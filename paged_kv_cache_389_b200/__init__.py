@@ -276,35 +276,22 @@ def pa_prefill_chunk(query, key_cache, value_cache, block_tables, context_lens, 
 
 
 # ------------------------------------------------ serving step: plan, 8-bit cache
-# These calls check that every tensor is on one CUDA device and launch there, on `stream`
-# or on that device's current stream.  The smallest of them take a few microseconds on the
-# GPU, so the checks are written for their cost (current_stream() alone takes 2 to 3 us; the
-# raw handle 0.1).
-def _run(fn, name, dev, stream, *args):
-    """Call the library's fn with the stream's handle appended, with device `dev` current."""
-    if dev < 0:
-        raise AssertionError("tensors passed to the library must be on a CUDA device")
-    cuda = _torch().cuda
-    handle = _torch()._C._cuda_getCurrentRawStream(dev) if stream is None else stream.cuda_stream
-    if dev == cuda.current_device():
-        status = fn(*args, handle)
-    else:
-        with cuda.device(dev):
-            status = fn(*args, handle)
-    if status != PA_OK:
-        raise PAError(status, name)
+# The checks of these calls (types, shapes, one CUDA device, where the launch then goes, on
+# `stream` or on that device's current stream) are compiled: the smallest of them take 4 us on
+# the GPU, and checks in Python with a ctypes call took 10 us (now 6 us a call, back to back).
+# A wrong tensor raises AssertionError.
+_binding = None
 
 
-def _p(t, dtype, shape, dev, what):
-    """Address of a contiguous tensor of this type and shape on device `dev`."""
-    if t.dtype != dtype or t.shape != shape or t.get_device() != dev or not t.is_contiguous():
-        raise AssertionError(f"{what}: contiguous {dtype} of shape {tuple(shape)} on device {dev} wanted, got {t.dtype} "
-                             f"{tuple(t.shape)} on {t.device}")
-    return t.data_ptr()
-
-
-def _flag(err_flag, dev):
-    return None if err_flag is None else _p(err_flag, _torch().int32, (1,), dev, "err_flag")
+def _load_binding():
+    global _binding
+    _torch()   # its libraries first
+    try:
+        from . import _step as module
+    except ImportError as e:
+        raise ImportError(f"{e}: build it with `python paged_kv_cache_389_b200/build.py`") from e
+    _binding = module
+    return module
 
 
 def pa_step_plan(counts, context_lens, block_tables, free_blocks, num_free, slot_mapping, seq_starts,
@@ -313,117 +300,52 @@ def pa_step_plan(counts, context_lens, block_tables, free_blocks, num_free, slot
     sequence.  counts, context_lens int32 [S]; block_tables int32 [S, max_blocks] (extended in
     place); free_blocks int32 [N] with its height num_free int32 [1]; out: slot_mapping int64
     [capacity], seq_starts int32 [S + 1], new_context_lens and new_num_free (default: in place)."""
-    i32, dev = _torch().int32, counts.get_device()
-    S, = counts.shape
-    mb = block_tables.shape[-1]
-    N, = free_blocks.shape
-    cap, = slot_mapping.shape
-    lens = _p(context_lens, i32, (S,), dev, "context_lens")
-    height = _p(num_free, i32, (1,), dev, "num_free")
-    _run(_lib.pa_step_plan, "pa_step_plan", dev, stream, _p(counts, i32, (S,), dev, "counts"), lens, S,
-         _p(block_tables, i32, (S, mb), dev, "block_tables"), mb, _p(free_blocks, i32, (N,), dev, "free_blocks"), N, height,
-         _p(slot_mapping, _torch().int64, (cap,), dev, "slot_mapping"), cap, _p(seq_starts, i32, (S + 1,), dev, "seq_starts"),
-         lens if new_context_lens is None else _p(new_context_lens, i32, (S,), dev, "new_context_lens"),
-         height if new_num_free is None else _p(new_num_free, i32, (1,), dev, "new_num_free"), _flag(err_flag, dev))
+    status = (_binding or _load_binding()).step_plan(counts, context_lens, block_tables, free_blocks, num_free, slot_mapping,
+                                               seq_starts, new_context_lens, new_num_free, err_flag, stream)
+    if status != PA_OK:
+        raise PAError(status, "pa_step_plan")
 
 
 def pa_step_release(finished, context_lens, block_tables, free_blocks, num_free, new_context_lens=None,
                     new_num_free=None, err_flag=None, stream=None):
     """Give the blocks of the sequences with finished[s] != 0 (int32 [S]) back to the stack."""
-    i32, dev = _torch().int32, finished.get_device()
-    S, = finished.shape
-    mb = block_tables.shape[-1]
-    N, = free_blocks.shape
-    lens = _p(context_lens, i32, (S,), dev, "context_lens")
-    height = _p(num_free, i32, (1,), dev, "num_free")
-    _run(_lib.pa_step_release, "pa_step_release", dev, stream, _p(finished, i32, (S,), dev, "finished"), lens, S,
-         _p(block_tables, i32, (S, mb), dev, "block_tables"), mb, _p(free_blocks, i32, (N,), dev, "free_blocks"), N, height,
-         lens if new_context_lens is None else _p(new_context_lens, i32, (S,), dev, "new_context_lens"),
-         height if new_num_free is None else _p(new_num_free, i32, (1,), dev, "new_num_free"), _flag(err_flag, dev))
-
-
-@functools.lru_cache(maxsize=64)
-def _scaled_desc(num_blocks, num_kv_heads, block_size, head_dim, code):
-    return CacheDesc(num_blocks, num_kv_heads, block_size, head_dim, code, 1.0, 1.0)
-
-
-def _scaled_pool(key_cache, value_cache, key_scales, value_scales, dev):
-    """(key codes, value codes, key scales, value scales, descriptor) of pools of
-    torch.float8_e4m3fn or torch.int8 codes with float32 scales [num_blocks, num_kv_heads]."""
-    torch = _torch()
-    dt, shape = key_cache.dtype, key_cache.shape
-    if dt == torch.float8_e4m3fn:
-        code = PA_FP8_E4M3
-    elif dt == torch.int8:
-        code = PA_INT8
-    else:
-        raise TypeError(f"unsupported dtype {dt}")
-    nb, hkv, bs, d = shape
-    return (_p(key_cache, dt, shape, dev, "key_cache"), _p(value_cache, dt, shape, dev, "value_cache"),
-            _p(key_scales, torch.float32, (nb, hkv), dev, "key_scales"),
-            _p(value_scales, torch.float32, (nb, hkv), dev, "value_scales"), C.byref(_scaled_desc(nb, hkv, bs, d, code)))
-
-
-def _rows(t, tokens, heads, d, dev, what):
-    """(address, elements between tokens) of bf16 [tokens, heads, d] whose heads and dims are
-    contiguous; the tokens may be further apart."""
-    st = t.stride()
-    if (t.dtype != _torch().bfloat16 or t.shape != (tokens, heads, d) or t.get_device() != dev or st[2] != 1
-            or (heads > 1 and st[1] != d)):
-        raise AssertionError(f"{what}: bf16 [{tokens}, {heads}, {d}] with contiguous heads and dims on device {dev} "
-                             f"wanted, got {t.dtype} {tuple(t.shape)} with strides {st} on {t.device}")
-    return t.data_ptr(), st[0] if tokens > 1 else heads * d
+    status = (_binding or _load_binding()).step_release(finished, context_lens, block_tables, free_blocks, num_free,
+                                                  new_context_lens, new_num_free, err_flag, stream)
+    if status != PA_OK:
+        raise PAError(status, "pa_step_release")
 
 
 def pa_cache_write_scaled(key, value, slot_mapping, key_cache, value_cache, key_scales, value_scales,
                           err_flag=None, stream=None):
     """Append key/value bf16 [T, Hkv, d] (tokens may be strided) at slot_mapping (int64 [T]) to
-    8-bit pools with a power-of-two scale per (block, kv head)."""
-    dev = key_cache.get_device()
-    kc, vc, ks, vs, desc = _scaled_pool(key_cache, value_cache, key_scales, value_scales, dev)
-    T = key.shape[0]
-    _, hkv, _, d = key_cache.shape
-    k, k_stride = _rows(key, T, hkv, d, dev, "key")
-    v, v_stride = _rows(value, T, hkv, d, dev, "value")
-    _run(_lib.pa_cache_write_scaled, "pa_cache_write_scaled", dev, stream, k, v, k_stride, v_stride,
-         _p(slot_mapping, _torch().int64, (T,), dev, "slot_mapping"), T, kc, vc, ks, vs, desc, _flag(err_flag, dev))
+    8-bit pools (torch.float8_e4m3fn or torch.int8 codes) with a power-of-two scale per (block,
+    kv head): key_scales, value_scales float32 [num_blocks, Hkv]."""
+    status = (_binding or _load_binding()).cache_write_scaled(key, value, slot_mapping, key_cache, value_cache, key_scales,
+                                                        value_scales, err_flag, stream)
+    if status != PA_OK:
+        raise PAError(status, "pa_cache_write_scaled")
 
 
 def pa_copy_blocks_scaled(key_cache, value_cache, key_scales, value_scales, src_dst_pairs, err_flag=None, stream=None):
     """Copy whole blocks, codes and scales, src -> dst for each row of int32 [P, 2]."""
-    dev = key_cache.get_device()
-    kc, vc, ks, vs, desc = _scaled_pool(key_cache, value_cache, key_scales, value_scales, dev)
-    P = src_dst_pairs.shape[0]
-    _run(_lib.pa_copy_blocks_scaled, "pa_copy_blocks_scaled", dev, stream, kc, vc, ks, vs,
-         _p(src_dst_pairs, _torch().int32, (P, 2), dev, "src_dst_pairs"), P, desc, _flag(err_flag, dev))
+    status = (_binding or _load_binding()).copy_blocks_scaled(key_cache, value_cache, key_scales, value_scales, src_dst_pairs,
+                                                        err_flag, stream)
+    if status != PA_OK:
+        raise PAError(status, "pa_copy_blocks_scaled")
 
 
 def pa_decode_scaled_workspace_size(num_q_heads, num_kv_heads, head_dim) -> int:
     return int(_lib.pa_decode_scaled_workspace_size(num_q_heads, num_kv_heads, head_dim))
 
 
-def _workspace(t, dev):
-    if t.get_device() != dev or not t.is_contiguous():
-        raise AssertionError("workspace: contiguous and on the other tensors' device")
-    return t.data_ptr(), t.numel() * t.element_size()
-
-
 def pa_decode_scaled(query, key_cache, value_cache, key_scales, value_scales, block_tables, context_lens,
                      max_context_len, scale, out, workspace, err_flag=None, stream=None):
     """Decode attention over 8-bit pools with a scale per (block, kv head); query/out bf16
     [S, Hq, d]; workspace of pa_decode_scaled_workspace_size(Hq, Hkv, d) bytes."""
-    torch, dev = _torch(), key_cache.get_device()
-    kc, vc, ks, vs, desc = _scaled_pool(key_cache, value_cache, key_scales, value_scales, dev)
-    shape = query.shape
-    S, hq, d = shape
-    if d != key_cache.shape[3]:
-        raise AssertionError("query: head_dim of the pools wanted")
-    mb = block_tables.shape[-1]
-    ws, ws_bytes = _workspace(workspace, dev)
-    _run(_lib.pa_decode_scaled, "pa_decode_scaled", dev, stream, _p(query, torch.bfloat16, shape, dev, "query"), kc, vc, ks, vs,
-         _p(block_tables, torch.int32, (S, mb), dev, "block_tables"), mb,
-         _p(context_lens, torch.int32, (S,), dev, "context_lens"), int(max_context_len), S, hq, float(scale), ws, ws_bytes,
-         _p(out, torch.bfloat16, shape, dev, "out"), desc, _flag(err_flag, dev))
+    status = (_binding or _load_binding()).decode_scaled(query, key_cache, value_cache, key_scales, value_scales, block_tables,
+                                                   context_lens, int(max_context_len), scale, out, workspace, err_flag, stream)
+    if status != PA_OK:
+        raise PAError(status, "pa_decode_scaled")
 
 
 def pa_prefill_packed_workspace_size(num_tokens, num_seqs, num_q_heads, num_kv_heads) -> int:
@@ -434,16 +356,10 @@ def pa_prefill_packed(query, key, value, seq_starts, max_seq_len, scale, out, wo
     """Causal attention over packed prompts; query/out bf16 [T, Hq, d], key/value [T, Hkv, d]
     (their tokens may be strided), seq_starts int32 [S + 1], workspace of
     pa_prefill_packed_workspace_size(T, S, Hq, Hkv) bytes."""
-    torch, dev = _torch(), query.get_device()
-    T, hq, d = query.shape
-    hkv, S = key.shape[1], seq_starts.shape[0] - 1
-    q, q_stride = _rows(query, T, hq, d, dev, "query")
-    k, k_stride = _rows(key, T, hkv, d, dev, "key")
-    v, v_stride = _rows(value, T, hkv, d, dev, "value")
-    ws, ws_bytes = _workspace(workspace, dev)
-    _run(_lib.pa_prefill_packed, "pa_prefill_packed", dev, stream, q, k, v, q_stride, k_stride, v_stride,
-         _p(seq_starts, torch.int32, (S + 1,), dev, "seq_starts"), S, T, int(max_seq_len), hq, hkv, d, float(scale), ws,
-         ws_bytes, _p(out, torch.bfloat16, (T, hq, d), dev, "out"), _flag(err_flag, dev))
+    status = (_binding or _load_binding()).prefill_packed(query, key, value, seq_starts, int(max_seq_len), scale, out, workspace,
+                                                    err_flag, stream)
+    if status != PA_OK:
+        raise PAError(status, "pa_prefill_packed")
 
 
 def pa_wait(err_flag=None, stream=None, timeout_ms: int = 10000) -> int:

@@ -1,5 +1,6 @@
 """Build ``libpa_b200.so`` in-tree: the sm_100a kernels, the C ABI and the host
-block manager, compiled with nvcc for ``-gencode arch=compute_100a,code=sm_100a``.
+block manager, compiled with nvcc for ``-gencode arch=compute_100a,code=sm_100a``;
+and ``_step.so``, the compiled binding of the serving-step calls (against torch's headers).
 
 ``python paged_kv_cache_389_b200/build.py [--force]`` (run as a script: importing the
 package needs the built library).  nvcc cross-compiles, so
@@ -20,6 +21,8 @@ CSRC = os.path.join(PKG, "csrc")
 HOST = os.path.join(PKG, "host")
 OBJ = os.path.join(PKG, "_build")
 LIB = os.path.join(PKG, "libpa_b200.so")
+BINDING = os.path.join(PKG, "binding", "step.cpp")
+STEP = os.path.join(PKG, "_step.so")
 
 NVCC = os.environ.get("NVCC", "/usr/local/cuda/bin/nvcc")
 ARCH = ["-gencode", "arch=compute_100a,code=sm_100a"]
@@ -56,9 +59,33 @@ def _compile(src: str, extra: list[str]) -> str:
     return obj
 
 
+def build_binding(force: bool = False) -> str:
+    """Compile the binding of the serving-step calls, linked to the library beside it."""
+    inputs = [BINDING, os.path.join(INCLUDE, "pa.h"), __file__]
+    if not force and os.path.exists(STEP) and all(os.path.getmtime(f) <= os.path.getmtime(STEP) for f in inputs):
+        return STEP
+    import sysconfig
+    import torch
+    from torch.utils import cpp_extension
+    tmp = STEP + f".tmp{os.getpid()}"
+    dirs = [INCLUDE] + cpp_extension.include_paths() + [os.path.join(os.path.dirname(os.path.dirname(NVCC)), "include"),
+                                                        sysconfig.get_paths()["include"]]
+    libs = cpp_extension.library_paths()
+    cmd = (["g++", "-O2", "-std=c++17", "-fPIC", "-shared", "-fvisibility=hidden", "-Wall",
+            f"-D_GLIBCXX_USE_CXX11_ABI={int(torch._C._GLIBCXX_USE_CXX11_ABI)}", BINDING, "-o", tmp, "-I" + dirs[0]]
+           + [x for d in dirs[1:] for x in ("-isystem", d)] + ["-L" + d for d in libs]
+           + ["-lc10", "-lc10_cuda", "-ltorch_cpu", "-ltorch_python", "-L" + PKG, "-l:" + os.path.basename(LIB), "-Wl,-rpath,$ORIGIN"])
+    r = subprocess.run(cmd, capture_output=True, text=True)
+    if r.returncode != 0:
+        raise RuntimeError(f"compile failed: {' '.join(cmd)}\n{r.stdout}\n{r.stderr}")
+    os.replace(tmp, STEP)
+    return STEP
+
+
 def build(force: bool = False, verbose_ptxas: bool = False) -> str:
-    """Compile every source and link the shared library; return its path."""
+    """Compile every source, link the shared library and the binding; return the library's path."""
     if not force and not _stale():
+        build_binding()
         return LIB
     os.makedirs(OBJ, exist_ok=True)
     extra = ["-Xptxas", "-v"] if verbose_ptxas else []
@@ -70,6 +97,7 @@ def build(force: bool = False, verbose_ptxas: bool = False) -> str:
     if r.returncode != 0:
         raise RuntimeError(f"link failed: {' '.join(cmd)}\n{r.stdout}\n{r.stderr}")
     os.replace(tmp, LIB)
+    build_binding(force)
     return LIB
 
 

@@ -240,3 +240,26 @@ def test_paged_cache_refuses_int8_without_block_scales(pa):
         PagedKVCache(4, 2, 64, torch.int8, device="cpu")
     with pytest.raises(ValueError):
         PagedKVCache(4, 2, 64, torch.bfloat16, device="cpu", block_scales=True)
+
+
+def test_binding_says_what_is_wrong(pa):
+    """Arguments that are no tensors, of another rank, type or shape, or numbers out of 32 bits: an
+    exception that names the argument, whatever the call."""
+    torch = torch_mod()
+    z = lambda *s, dt=torch.int32: torch.zeros(*s, dtype=dt)
+    right = dict(counts=z(2), context_lens=z(2), block_tables=z(2, 3), free_blocks=z(8), num_free=z(1),
+                 slot_mapping=z(4, dt=torch.int64), seq_starts=z(3), new_context_lens=z(2), new_num_free=z(1), err_flag=z(1))
+    for name, bad in (("counts", z(2, 1)), ("context_lens", z(3)), ("block_tables", z(2)), ("free_blocks", z(8, dt=torch.int64)),
+                      ("num_free", z(2)), ("slot_mapping", z(4)), ("seq_starts", z(2, 2)[:, 0]), ("new_context_lens", z(1)),
+                      ("new_num_free", z(1, 1)), ("err_flag", z(1, dt=torch.int64))):
+        with pytest.raises(AssertionError, match=name):
+            pa.pa_step_plan(**{**right, name: bad})
+        with pytest.raises(TypeError, match=name):
+            pa.pa_step_plan(**{**right, name: 3})
+    q, k, ws = torch.zeros(4, 2, 64, dtype=torch.bfloat16), torch.zeros(4, 1, 64, dtype=torch.bfloat16), z(64)
+    with pytest.raises(AssertionError, match="max_seq_len"):
+        pa.pa_prefill_packed(q, k, k, z(2), 2 ** 31, 0.1, q.clone(), ws)
+    with pytest.raises(AssertionError, match="seq_starts"):
+        pa.pa_prefill_packed(q, k, k, z(0), 4, 0.1, q.clone(), ws)
+    with pytest.raises(TypeError):
+        pa.pa_prefill_packed(q, k, k, z(2), 4, "0.1", q.clone(), ws)
