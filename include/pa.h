@@ -450,7 +450,8 @@ PA_API size_t pa_prefill_packed_workspace_size(int32_t num_tokens, int32_t num_s
  * tcgen05 tensor-core tiles, bf16 operands, fp32 accumulation, softmax statistics and
  * sums; probabilities are rounded to bf16 for the product with V.  Two kernels (the
  * first lists the jobs from the lengths, in `workspace`, whose contents need not be set;
- * calls that overlap on the GPU need workspaces of their own).  Replays correctly from a
+ * calls that overlap on the GPU need workspaces of their own), or one for a few short
+ * sequences (max_seq_len * num_q_heads / num_kv_heads <= 256).  Replays correctly from a
  * graph, following seq_starts.
  * Source: chenxutan 2.3 (prefill computes the whole prompt, compute bound).
  */

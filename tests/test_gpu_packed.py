@@ -181,6 +181,32 @@ def test_bad_starts_are_flagged(pa):
 
 
 @pytest.mark.gpu
+@pytest.mark.parametrize("hq,hkv,d", [(4, 4, 64), (8, 1, 128), (8, 2, 64)])
+@pytest.mark.parametrize("seqs", [40, 3000])
+def test_short_sequences_without_a_list(pa, hq, hkv, d, seqs):
+    """Sequences of at most one pair of row tiles (empty ones and the longest among them), few
+    enough to be taken in turn and too many for that; then with bad ones between them."""
+    torch = torch_mod()
+    rng = np.random.default_rng(hq + d)
+    most = 256 // (hq // hkv)
+    n = rng.integers(0, most if seqs < 100 else 6, seqs, endpoint=True)
+    n[3], n[7], n[-1] = most, 0, 1
+    starts = np.concatenate([[2], 2 + np.cumsum(n)])
+    q, k, v = inputs(rng, int(starts[-1]) + 3, hq, hkv, d, True)
+    out, flag = run(pa, q, k, v, starts, 0.11, most)
+    assert flag == 0
+    check(out, q, k, v, starts, 0.11)
+    # sequences of that length (the fourth, and any other) are longer than announced: left out
+    full = run(pa, q, k, v, starts, 0.11, most)[0]
+    out, flag = run(pa, q, k, v, starts, 0.11, most - 1)
+    assert flag == pa.PA_DEVERR_CHUNK
+    for s in np.nonzero(n == most)[0]:
+        assert (out[starts[s]:starts[s + 1]] == 7).all()
+        out[starts[s]:starts[s + 1]] = full[starts[s]:starts[s + 1]]
+    check(out, q, k, v, starts, 0.11)
+
+
+@pytest.mark.gpu
 @pytest.mark.parametrize("tokens,seqs,hq", [(300, 40, 4), (32 * (2 ** 19 + 1), 16384, 8)])
 def test_starts_that_go_back_and_forth_list_nothing(pa, tokens, seqs, hq):
     """Starts 0, T, 0, T, ...: every second sequence is all of the rows.  Their pairs do not fit
