@@ -101,6 +101,8 @@ struct Tiles {
 };
 constexpr uint32_t kQHalf = kTile * 128;   // 64 columns of a 128-row tile in shared memory
 
+constexpr int kJobSlots = 8;         // job records in shared memory
+
 enum Bar {
     // A job of n key tiles uses n + 1 slots of the K/V ring; slot i holds K(i) and V(i - 1): what
     // the products between two softmax steps read, under one barrier.
@@ -116,7 +118,8 @@ enum Bar {
     kBarOFull = kBarPFree + 2,           // [2] the job's last PV_t is done
     kBarOFree = kBarOFull + 2,           // [2] O_t has been read (128 threads)
     kBarIdle = kBarOFree + 2,            // [2] every MMA of a stream has completed
-    kNumBars = kBarIdle + 2
+    kBarRead = kBarIdle + 2,             // [kJobSlots] the slot's job has been read by every softmax warp
+    kNumBars = kBarRead + kJobSlots
 };
 
 template <int D>
@@ -360,7 +363,7 @@ __global__ void __launch_bounds__(kThreads, 1) packed_prefill_kernel(const __gri
             const bool rows = (i >= kBarSRead && i < kBarSRead + 2) || (i >= kBarPFull && i < kBarPFull + 2) ||
                               (i >= kBarOFree && i < kBarOFree + 2);
             const bool both = i < kBarVLand || i == kBarQEmpty;
-            mbar_init(&bars[i], rows ? 128 : both ? 2 : 1);
+            mbar_init(&bars[i], rows ? 128 : i >= kBarRead ? 8 : both ? 2 : 1);
         }
         *abort_flag = 0;
         mbar_init_fence();
@@ -435,6 +438,10 @@ __global__ void __launch_bounds__(kThreads, 1) packed_prefill_kernel(const __gri
                             break;
                         }
                     }
+                    // A stream without rows in a job does not hold the others up, so a softmax warp
+                    // may be jobs behind: its record has to stay until it has read it.
+                    if (k >= kJobSlots) ok = wait_bar(&bars[kBarRead + (k & 7)], ((k >> 3) - 1) & 1, abort_flag, p);
+                    if (!ok) break;
                     job_rec[(k & 7) * 4] = rec.x;
                     job_rec[(k & 7) * 4 + 1] = rec.y;
                     job_rec[(k & 7) * 4 + 2] = rec.z;
@@ -614,6 +621,8 @@ __global__ void __launch_bounds__(kThreads, 1) packed_prefill_kernel(const __gri
         bool live = true;
         Job jb;
         for (int k = 0; live && read_job_warp(k, jb); ++k) {
+            __syncwarp();
+            if (lane == 0) mbar_arrive(&bars[kBarRead + (k & 7)]);
             if (jb.ntiles[t] == 0) continue;
             const bool row_ok = r < jb.nrows[t];
             const int tok = jb.i0 + t * kTok + r / G;        // token within the sequence

@@ -207,6 +207,29 @@ def test_short_sequences_without_a_list(pa, hq, hkv, d, seqs):
 
 
 @pytest.mark.gpu
+@pytest.mark.parametrize("seqs", [2000, 4000])
+def test_a_stream_far_behind_the_other(pa, seqs):
+    """Rows that are computed again (masked infinities) keep one stream of a CTA busy while the
+    other goes through dozens of short sequences: their records have to wait for the slow one."""
+    rng = np.random.default_rng(4)
+    n = np.concatenate([[256] * 8, rng.integers(1, 4, seqs - 8)])
+    starts = np.concatenate([[0], np.cumsum(n)])
+    q, k, v = inputs(rng, int(starts[-1]), 1, 1, 64, False)
+    v[starts[1:9] - 1] = float("inf")     # seen by the last row only
+    out, flag = run(pa, q, k, v, starts, 0.125)
+    assert flag == 0
+    assert np.isinf(out[starts[1:9] - 1].double().cpu().numpy()).all()
+    out[starts[1:9] - 1] = 0
+    v[starts[1:9] - 1] = 0
+    mask = np.zeros(len(q), bool)
+    mask[starts[1:9] - 1] = True
+    f = lambda x: x.double().cpu().numpy()
+    o, mass, reach = step_ops.packed_attention(f(q), f(k), f(v), starts, 0.125)
+    far = np.abs(f(out) - o) - step_ops.attention_bound(o, mass, reach, (0, 2.0 ** -8, 0.0))
+    assert (far[~mask] <= 0).all()
+
+
+@pytest.mark.gpu
 @pytest.mark.parametrize("tokens,seqs,hq", [(300, 40, 4), (32 * (2 ** 19 + 1), 16384, 8)])
 def test_starts_that_go_back_and_forth_list_nothing(pa, tokens, seqs, hq):
     """Starts 0, T, 0, T, ...: every second sequence is all of the rows.  Their pairs do not fit
