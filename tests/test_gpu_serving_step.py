@@ -189,3 +189,72 @@ def test_calls_on_a_stream_of_their_own(pa):
         results.append(outs)
     for a, b in zip(*results):
         assert torch.equal(a, b)
+
+
+@pytest.mark.parametrize("code", CODES)
+def test_captured_steps_follow_the_device(pa, code):
+    """A prompt step and a decode step, each captured once (with one workspace between them) on a
+    side stream and replayed with other counts, rows and finished sequences, against the same
+    steps called one by one: every table, slot, code, scale and output the same, bit for bit."""
+    torch = torch_mod()
+    rng = np.random.default_rng(21)
+    hq, hkv, d, S, N, mb, cap = 8, 2, 128, 5, 96, 20, 500
+    order = torch.from_numpy(rng.permutation(N).astype(np.int32)).cuda()
+
+    class State:
+        def __init__(self):
+            z = lambda *s, dt=torch.int32: torch.zeros(*s, dtype=dt, device="cuda")
+            self.counts, self.done, self.lens, self.nf, self.err = z(S), z(S), z(S), z(1) + N, z(1)
+            self.tables, self.free = z(S, mb) - 1, order.clone()
+            self.slots, self.starts = z(cap, dt=torch.int64), z(S + 1)
+            self.kc, self.vc = (torch.zeros(N, hkv, 16, d, device="cuda").to(code_dtype(code)) for _ in range(2))
+            self.ks, self.vs = (torch.full((N, hkv), float("nan"), device="cuda") for _ in range(2))
+            self.x, self.q = rows(rng, cap, hq + 2 * hkv, d), rows(rng, S, hq, d)
+            self.out, self.dec = torch.zeros(cap, hq, d, dtype=torch.bfloat16, device="cuda"), torch.zeros_like(self.q)
+            self.ws = torch.empty(max(pa.pa_decode_scaled_workspace_size(hq, hkv, d),
+                                      pa.pa_prefill_packed_workspace_size(cap, S, hq, hkv)), dtype=torch.uint8, device="cuda")
+
+        def step(self, prompts):
+            q, k, v = self.x.split([hq, hkv, hkv], 1)
+            pa.pa_step_release(self.done, self.lens, self.tables, self.free, self.nf, err_flag=self.err)
+            pa.pa_step_plan(self.counts, self.lens, self.tables, self.free, self.nf, self.slots, self.starts, err_flag=self.err)
+            if prompts:
+                pa.pa_prefill_packed(q, k, v, self.starts, 300, 0.09, self.out, self.ws, self.err)
+            pa.pa_cache_write_scaled(k, v, self.slots, self.kc, self.vc, self.ks, self.vs, self.err)
+            pa.pa_decode_scaled(self.q, self.kc, self.vc, self.ks, self.vs, self.tables, self.lens, mb * 16, 0.09, self.dec,
+                                self.ws, self.err)
+
+    twin, state = State(), State()
+    scratch = State()
+    for prompts in (True, False):        # libraries and attributes set up before the capture
+        scratch.step(prompts)
+    torch.cuda.synchronize()
+    graphs = {}
+    side = torch.cuda.Stream()
+    for prompts in (True, False):
+        graphs[prompts] = torch.cuda.CUDAGraph()
+        with torch.cuda.graph(graphs[prompts], stream=side):
+            state.step(prompts)
+    for prompts, counts, done in ((True, [33, 1, 300, 0, 16], [0, 0, 0, 0, 0]), (False, [1, 1, 1, 0, 1], [0, 0, 0, 0, 0]),
+                                  (False, [1, 1, 1, 0, 1], [0, 0, 0, 0, 0]), (True, [0, 0, 250, 190, 0], [0, 0, 1, 0, 0]),
+                                  (False, [1, 1, 1, 1, 1], [0, 1, 0, 0, 0]), (False, [5, 0, 2, 1, 20], [0, 0, 0, 0, 0])):
+        x, q = rows(rng, cap, hq + 2 * hkv, d), rows(rng, S, hq, d)
+        for s in (twin, state):
+            s.counts.copy_(torch.tensor(counts))
+            s.done.copy_(torch.tensor(done))
+            s.x.copy_(x)
+            s.q.copy_(q)
+        twin.step(prompts)
+        graphs[prompts].replay()
+        torch.cuda.synchronize()
+        assert int(twin.err) == 0 and int(state.err) == 0
+        T = int(twin.starts[-1])
+        assert T == sum(counts)
+        for name in ("lens", "nf", "tables", "free", "slots", "starts", "dec"):
+            assert torch.equal(getattr(twin, name), getattr(state, name)), name
+        if prompts:
+            assert torch.equal(twin.out[:T], state.out[:T])
+        for name in ("kc", "vc"):
+            assert torch.equal(getattr(twin, name).view(torch.uint8), getattr(state, name).view(torch.uint8)), name
+        for name in ("ks", "vs"):
+            assert torch.equal(getattr(twin, name).nan_to_num(7), getattr(state, name).nan_to_num(7)), name
