@@ -17,8 +17,12 @@
 // share the writing.  The cluster barrier between reading and writing is what lets
 // the new lengths and the new stack height go where the old ones are (a captured
 // graph replays the step in place).  Few slots: one CTA, no cluster.  Measured in a graph: 256
-// sequences with a token each 4.2 us, 64 prompts with 69 thousand tokens 8.8 us (7.2 with a
-// cluster of 16, a size that not every device has).
+// sequences with a token each 4.2 us; 64 prompts with 4, 33, 66, 260 thousand slots 4.6, 6.0, 8.0,
+// 20.4 us with a cluster of 8 CTAs, 4.7, 5.2, 6.1, 12.0 with 16 (16 thousand: 4.9 with either), so
+// calls with more than 16 thousand take 16, a size above the portable one, where the device can
+// hold it.
+#include <atomic>
+
 #include <cooperative_groups.h>
 
 #include "pa_common.cuh"
@@ -31,6 +35,8 @@ namespace {
 constexpr unsigned kFull = 0xffffffffu;
 constexpr int kPlanThreads = 1024;
 constexpr int kPlanCluster = 8;       // portable cluster size
+constexpr int kPlanClusterBig = 16;   // where the device can hold one
+constexpr int64_t kBigWork = 16384;   // slots or table entries: one for each of their threads
 constexpr uint32_t kSat = 1u << 30;   // sums at or above it are "too many"
 
 __device__ __forceinline__ uint32_t sat_add(uint32_t a, uint32_t b) { return min(a + b, kSat); }
@@ -200,6 +206,39 @@ __global__ void __launch_bounds__(kPlanThreads, 1) step_plan_kernel(const StepPl
     }
 }
 
+// Whether the device can hold a cluster of kPlanClusterBig CTAs of this kernel with its most
+// shared memory (above the portable size, so it is asked; once per device).
+template <bool kRelease>
+bool big_cluster() {
+    constexpr int kDevices = 64;
+    static std::atomic<int> known[kDevices];   // 0: not asked, 1: no, 2: yes
+    int dev = 0;
+    if (cudaGetDevice(&dev) != cudaSuccess || dev < 0 || dev >= kDevices) return false;
+    int k = known[dev].load(std::memory_order_relaxed);
+    if (k == 0) {
+        const auto kern = step_plan_kernel<kRelease, true>;
+        const int smem = 3 * (kMaxPlanSeqs + 1) * 4;
+        int clusters = 0;
+        cudaLaunchConfig_t cfg = {};
+        cfg.gridDim = dim3(kPlanClusterBig);
+        cfg.blockDim = dim3(kPlanThreads);
+        cfg.dynamicSmemBytes = (size_t)smem;
+        cudaLaunchAttribute attr[1];
+        attr[0].id = cudaLaunchAttributeClusterDimension;
+        attr[0].val.clusterDim.x = kPlanClusterBig;
+        attr[0].val.clusterDim.y = attr[0].val.clusterDim.z = 1;
+        cfg.attrs = attr;
+        cfg.numAttrs = 1;
+        const bool yes = cudaFuncSetAttribute(kern, cudaFuncAttributeNonPortableClusterSizeAllowed, 1) == cudaSuccess &&
+                         cudaFuncSetAttribute(kern, cudaFuncAttributeMaxDynamicSharedMemorySize, smem) == cudaSuccess &&
+                         cudaOccupancyMaxActiveClusters(&clusters, kern, &cfg) == cudaSuccess && clusters > 0;
+        if (!yes) (void)cudaGetLastError();
+        k = yes ? 2 : 1;
+        known[dev].store(k, std::memory_order_relaxed);
+    }
+    return k == 2;
+}
+
 template <bool kRelease, bool kCluster>
 cudaError_t launch(const StepPlan &p, int ctas, cudaStream_t stream) {
     const size_t smem = (size_t)(3 * (p.num_seqs + 1)) * 4;
@@ -216,7 +255,7 @@ cudaError_t launch(const StepPlan &p, int ctas, cudaStream_t stream) {
     cfg.stream = stream;
     cudaLaunchAttribute attr[1];
     attr[0].id = cudaLaunchAttributeClusterDimension;
-    attr[0].val.clusterDim.x = kCluster ? kPlanCluster : 1;
+    attr[0].val.clusterDim.x = (unsigned)ctas;
     attr[0].val.clusterDim.y = attr[0].val.clusterDim.z = 1;
     cfg.attrs = attr;
     cfg.numAttrs = 1;
@@ -228,10 +267,10 @@ cudaError_t launch(const StepPlan &p, int ctas, cudaStream_t stream) {
 cudaError_t launch_step_plan(const StepPlan &p, bool release, cudaStream_t stream) {
     // What the writers share out: slots (plan) or at most every table entry (release).
     const int64_t work = release ? (int64_t)p.num_seqs * p.max_blocks : (int64_t)p.slot_capacity;
-    const bool cluster = work > 2 * kPlanThreads;
-    if (release)
-        return cluster ? launch<true, true>(p, kPlanCluster, stream) : launch<true, false>(p, 1, stream);
-    return cluster ? launch<false, true>(p, kPlanCluster, stream) : launch<false, false>(p, 1, stream);
+    if (work <= 2 * kPlanThreads)
+        return release ? launch<true, false>(p, 1, stream) : launch<false, false>(p, 1, stream);
+    if (release) return launch<true, true>(p, work > kBigWork && big_cluster<true>() ? kPlanClusterBig : kPlanCluster, stream);
+    return launch<false, true>(p, work > kBigWork && big_cluster<false>() ? kPlanClusterBig : kPlanCluster, stream);
 }
 
 }  // namespace pa

@@ -128,6 +128,21 @@ def test_a_step_that_does_not_fit_changes_nothing(pa, fault, big):
 
 
 @pytest.mark.gpu
+@pytest.mark.parametrize("S,count_hi,pad", [(64, 500, 16000), (3, 9000, 9001), (5000, 8, 40001), (16384, 2, 70000)])
+def test_plan_of_many_slots(pa, S, count_hi, pad):
+    """Above the size at which a larger cluster shares the writing, in place and not."""
+    rng = np.random.default_rng(S)
+    c = case(rng, S, count_hi, 70, pad=pad)
+    ref = step_ops.step_plan(*c)
+    assert len(ref[1]) > 16384
+    for inplace, offset in ((False, 0), (True, 1), (True, 0)):
+        got, flag = run_plan(pa, *c, inplace, offset)
+        assert flag == 0
+        for g, r, what in zip(got, ref, ("tables", "slots", "starts", "lens", "num_free")):
+            assert np.array_equal(g, r), what
+
+
+@pytest.mark.gpu
 def test_lengths_next_to_2_31(pa):
     """A table row of more than 2^31 tokens: lengths stop at what 32 bits hold."""
     torch = torch_mod()
@@ -197,7 +212,7 @@ def test_a_run_of_steps_follows_the_host_manager(pa):
 
 
 @pytest.mark.gpu
-@pytest.mark.parametrize("S,mb", [(0, 4), (1, 1), (40, 9), (3000, 3)])
+@pytest.mark.parametrize("S,mb", [(0, 4), (1, 1), (40, 9), (3000, 3), (3000, 20)])
 def test_release(pa, S, mb):
     torch = torch_mod()
     rng = np.random.default_rng(S + mb)
