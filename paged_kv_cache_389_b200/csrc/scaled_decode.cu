@@ -59,7 +59,6 @@ constexpr int kWarps = 12;
 constexpr int kThreads = kWarps * 32;
 constexpr float kLazy = 256.f;        // p and w may grow to 2^8 before the reference points move
 constexpr int kMaxCum = 8192;         // prefix-sum entries in shared memory (every k-th sequence beyond)
-constexpr int kMinItems = 2;          // items a warp takes at least (fewer CTAs for tiny batches)
 constexpr int kWholeItems = 33;       // longest segments that stay within a CTA
 constexpr int kMergeThreads = 256;
 
@@ -515,7 +514,9 @@ __global__ void __launch_bounds__(kThreads, 1) decode_scaled_kernel(const __grid
     }
     const int64_t total = (int64_t)cum[ncum] * hkv;
     const int64_t workers = (int64_t)gridDim.x * kWarps;
-    const int64_t per = max((int64_t)kMinItems, (total + workers - 1) / workers);
+    // down to one item a warp: four sequences of 17 to 100 tokens take 7.9 us, with at least 2, 4, 8
+    // items 9.0, 9.9, 12.1
+    const int64_t per = (total + workers - 1) / workers;
     int64_t cta0 = min(total, (int64_t)blockIdx.x * kWarps * per), cta1 = min(total, cta0 + kWarps * per);
     int64_t warp_items = per;
     if (p.whole) {   // both ends move up to where a segment begins
@@ -758,7 +759,7 @@ cudaError_t launch(Params &p, void *workspace, int ctas, cudaStream_t stream) {
     if (e != cudaSuccess) return e;
     // Segments of at most kWholeItems items (496 tokens) stay within a CTA, which costs a CTA
     // at most one segment more than its share and saves the second kernel (four
-    // sequences of 17 to 100 tokens: 9.1 us against 9.6 in a graph).
+    // sequences of 17 to 100 tokens: 9.1 us against 9.6 in a graph, at two items a warp).
     p.whole = p.max_context / kBlockSize + 2 <= kWholeItems;
     decode_scaled_kernel<D, G, kInt8><<<(unsigned)ctas, kThreads, L::bytes(ncum + 1), stream>>>(p);
     if ((e = cudaGetLastError()) != cudaSuccess || p.whole) return e;
