@@ -258,3 +258,52 @@ def test_captured_steps_follow_the_device(pa, code):
             assert torch.equal(getattr(twin, name).view(torch.uint8), getattr(state, name).view(torch.uint8)), name
         for name in ("ks", "vs"):
             assert torch.equal(getattr(twin, name).nan_to_num(7), getattr(state, name).nan_to_num(7)), name
+
+
+def test_calls_that_overlap(pa):
+    """Packed attention and 8-bit decodes on three streams at once, each with a workspace of its
+    own: the results of the same calls one after the other, bit for bit."""
+    torch = torch_mod()
+    rng = np.random.default_rng(33)
+    hq, hkv, d, S = 8, 2, 64, 40
+    n = rng.integers(1, 700, S)
+    starts = torch.from_numpy(np.concatenate([[0], np.cumsum(n)]).astype(np.int32)).cuda()
+    T = int(starts[-1])
+    q, k, v = rows(rng, T, hq + 2 * hkv, d).split([hq, hkv, hkv], 1)
+    blocks = -(-n // 16)
+    N = int(blocks.sum())
+    tables = np.full((S, int(blocks.max())), -1, np.int32)
+    ids, at = rng.permutation(N), 0
+    for s in range(S):
+        tables[s, :blocks[s]] = ids[at:at + blocks[s]]
+        at += blocks[s]
+    slots = np.concatenate([tables[s, np.arange(n[s]) // 16].astype(np.int64) * 16 + np.arange(n[s]) % 16 for s in range(S)])
+    tables, lens = torch.from_numpy(tables).cuda(), torch.from_numpy(n.astype(np.int32)).cuda()
+    kc, vc = (torch.zeros(N, hkv, 16, d, dtype=torch.int8, device="cuda") for _ in range(2))
+    ks, vs = (torch.zeros(N, hkv, device="cuda") for _ in range(2))
+    err = torch.zeros(1, dtype=torch.int32, device="cuda")
+    pa.pa_cache_write_scaled(k, v, torch.from_numpy(slots).cuda(), kc, vc, ks, vs, err)
+    qd = rows(rng, S, hq, d)
+
+    def attend(stream, out, ws):
+        pa.pa_prefill_packed(q, k, v, starts, 700, 0.125, out, ws, err, stream)
+
+    def decode(stream, out, ws):
+        pa.pa_decode_scaled(qd, kc, vc, ks, vs, tables, lens, int(n.max()), 0.125, out, ws, err, stream)
+
+    size = max(pa.pa_prefill_packed_workspace_size(T, S, hq, hkv), pa.pa_decode_scaled_workspace_size(hq, hkv, d))
+    ws = [torch.empty(size, dtype=torch.uint8, device="cuda") for _ in range(3)]
+    want = torch.zeros_like(q.contiguous()), torch.zeros_like(qd)
+    attend(None, want[0], ws[0])
+    decode(None, want[1], ws[0])
+    torch.cuda.synchronize()
+    streams = [torch.cuda.Stream() for _ in range(3)]
+    for _ in range(10):
+        got = [torch.zeros_like(want[0]), torch.zeros_like(want[1]), torch.zeros_like(want[1])]
+        torch.cuda.synchronize()
+        for _ in range(4):
+            for call, stream, out, w in zip((attend, decode, decode), streams, got, ws):
+                call(stream, out, w)
+        torch.cuda.synchronize()
+        assert torch.equal(got[0], want[0]) and torch.equal(got[1], want[1]) and torch.equal(got[2], want[1])
+    assert int(err) == 0
