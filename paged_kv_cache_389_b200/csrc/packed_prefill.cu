@@ -160,7 +160,7 @@ struct PlanParams {
     int4 *jobs;
     int32_t *meta;
     int32_t *err;
-    int32_t num_seqs, num_tokens, max_len, pair_tokens, max_jobs;
+    int32_t num_seqs, num_tokens, max_len, pair_tokens, max_jobs;   // 1 <= max_len <= num_tokens
 };
 
 // ---------------------------------------------------------------- the job list
@@ -234,8 +234,8 @@ __global__ void __launch_bounds__(kPlanThreads, 1) packed_plan_kernel(const Plan
     if (bad || (!fits && threadIdx.x == 0)) flag_error(p.err, PA_DEVERR_CHUNK);
     __syncthreads();
     if (!fits) total = 0;
-    const int most = (p.max_len + p.pair_tokens - 1) / p.pair_tokens;
-    auto bucket_of = [&](int jp) { return kBuckets - 1 - (int)((int64_t)jp * kBuckets / max(most, 1)); };
+    const int most = (p.max_len - 1) / p.pair_tokens + 1;   // pairs of the longest sequence: jp < most
+    auto bucket_of = [&](int jp) { return kBuckets - 1 - (int)((int64_t)jp * kBuckets / most); };
     auto seq_of = [&](int e) {
         int lo = 0, hi = S;
         while (hi - lo > 1) {
@@ -846,6 +846,8 @@ size_t packed_workspace(int32_t num_tokens, int32_t num_seqs, int32_t g) {
 cudaError_t launch_prefill_packed(const PackedPrefill &a, cudaStream_t stream) {
     const int g = a.num_q_heads / a.num_kv_heads, d = a.head_dim;
     const int64_t jobs = max_jobs(a.num_tokens, a.num_seqs, g);
+    // no sequence has more tokens than there are rows, whatever the caller's upper bound is
+    const int32_t max_len = std::min(a.max_seq_len, a.num_tokens);
     if (jobs * a.num_kv_heads >= kManyPairs) return cudaErrorNotSupported;
     PlanParams pl;
     pl.starts = a.starts;
@@ -854,7 +856,7 @@ cudaError_t launch_prefill_packed(const PackedPrefill &a, cudaStream_t stream) {
     pl.err = a.err;
     pl.num_seqs = a.num_seqs;
     pl.num_tokens = a.num_tokens;
-    pl.max_len = a.max_seq_len;
+    pl.max_len = max_len;
     pl.pair_tokens = 2 * kTile / g;
     pl.max_jobs = (int32_t)jobs;
     Params p;
@@ -880,7 +882,7 @@ cudaError_t launch_prefill_packed(const PackedPrefill &a, cudaStream_t stream) {
     p.scale_log2 = a.scale * kLog2e;
     p.num_seqs = a.num_seqs;
     p.num_tokens = a.num_tokens;
-    p.max_len = a.max_seq_len;
+    p.max_len = max_len;
     p.wait_ns = wait_limit_ns();
     int dev = 0;
     cudaError_t e = cudaGetDevice(&dev);
@@ -891,7 +893,7 @@ cudaError_t launch_prefill_packed(const PackedPrefill &a, cudaStream_t stream) {
     // (1.3 and 2.2 jobs a CTA); with more jobs handing them out evens the CTAs (22 a CTA: 87 us
     // with the list, 89 without; 108: 392 and 416).
     const int64_t direct = (int64_t)a.num_seqs * a.num_kv_heads;
-    if (a.max_seq_len <= pl.pair_tokens && direct <= (int64_t)kDirectJobs * num_sms(dev)) {
+    if (max_len <= pl.pair_tokens && direct <= (int64_t)kDirectJobs * num_sms(dev)) {
         p.starts = a.starts;
         const int grid = (int)std::min<int64_t>(direct, num_sms(dev));
         return d == 128 ? launch_group<128>(p, g, grid, stream) : launch_group<64>(p, g, grid, stream);

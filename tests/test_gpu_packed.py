@@ -308,3 +308,17 @@ def test_waits_that_run_out(pa):
     out, flag = run(pa, q, k, v, [0, 600], 0.1)
     assert flag == 0
     check(out, q, k, v, np.array([0, 600]), 0.1)
+
+
+@pytest.mark.gpu
+@pytest.mark.parametrize("hq,hkv,d", [(4, 4, 64), (8, 1, 128)])
+@pytest.mark.parametrize("top", [2 ** 31 - 1, 2 ** 31 - 31, 2 ** 30, 1401])
+def test_an_upper_bound_far_above_the_lengths(pa, hq, hkv, d, top):
+    """max_seq_len only bounds the lengths: any larger number, up to the largest of 32 bits, gives
+    the same rows, where jobs are listed and where short sequences are taken in turn."""
+    rng = np.random.default_rng(hq)
+    for starts in ((0, 1400), (0, 700, 701, 1300), (0, 20, 31)):
+        q, k, v = inputs(rng, starts[-1], hq, hkv, d, True)
+        out, flag = run(pa, q, k, v, starts, 0.1, top)
+        assert flag == 0
+        check(out, q, k, v, np.array(starts), 0.1)
