@@ -242,7 +242,8 @@ bool big_cluster() {
 template <bool kRelease, bool kCluster>
 cudaError_t launch(const StepPlan &p, int ctas, cudaStream_t stream) {
     const size_t smem = (size_t)(3 * (p.num_seqs + 1)) * 4;
-    if (smem > 48 * 1024) {   // above what a launch may ask for anyway
+    // The 48 KB that a launch may ask for anyway hold the kernel's static arrays too (272 bytes).
+    if (smem > 47 * 1024) {
         const cudaError_t e = cudaFuncSetAttribute(step_plan_kernel<kRelease, kCluster>,
                                                    cudaFuncAttributeMaxDynamicSharedMemorySize,
                                                    3 * (kMaxPlanSeqs + 1) * 4);

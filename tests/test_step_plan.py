@@ -1,12 +1,19 @@
 """The step plan on the GPU (block tables, slots, starts from lengths) against the
 definition and against the host block manager, and the refusals."""
 import ctypes as C
+import os
+import subprocess
+import sys
+import threading
+import time
 
 import numpy as np
 import pytest
 
 from oracle import step_ops
 from test_abi import _gpu_visible
+
+ROOT = os.path.dirname(os.path.dirname(os.path.abspath(__file__)))
 
 
 def torch_mod():
@@ -278,3 +285,40 @@ def test_binding_says_what_is_wrong(pa):
         pa.pa_prefill_packed(q, k, k, z(0), 4, 0.1, q.clone(), ws)
     with pytest.raises(TypeError):
         pa.pa_prefill_packed(q, k, k, z(2), 4, "0.1", q.clone(), ws)
+
+
+# Kernel attributes last for the process, and one set by a larger call would hide a launch that asks for
+# more shared memory than it may: a process of its own, sizes ascending, one kernel variant after the other.
+AROUND_48_KB = """
+import sys
+import numpy as np
+sys.path[:0] = ["tests", "."]
+import paged_kv_cache_389_b200 as pa
+import test_step_plan as t
+from oracle import step_ops
+for pad in (0, 4096):                      # one CTA (a few slots), a cluster
+    for S in (4071, 4072, 4073, 4080, 4095, 4096, 4097):
+        c = list(t.case(np.random.default_rng(S), S, 1, 20))
+        c[0][:] = 0
+        c[0][:1500] = 1
+        c[5] = 1500 + pad
+        ref = step_ops.step_plan(*c)
+        got, flag = t.run_plan(pa, *c, False)
+        assert flag == 0 and all(np.array_equal(g, r) for g, r in zip(got, ref)), (pad, S)
+for S in (4071, 4072, 4073, 4080, 4095, 4096, 4097):
+    fin, lens = np.ones(S, np.int32), np.full(S, 9, np.int32)
+    tables = t.dev(np.arange(S, dtype=np.int32)[:, None])
+    free, nf, err, l = t.dev(np.full(S, -5, np.int32)), t.dev(np.zeros(1, np.int32)), t.dev(np.zeros(1, np.int32)), t.dev(lens)
+    pa.pa_step_release(t.dev(fin), l, tables, free, nf, err_flag=err)
+    assert pa.pa_wait(err) == 0 and int(nf) == S and free.tolist() == list(range(S)), S
+    assert (tables == -1).all() and (l == 0).all()
+print("all sizes")
+"""
+
+
+@pytest.mark.gpu
+def test_sizes_around_48_kb_of_shared_memory(pa):
+    """12 (S + 1) bytes for the lengths and sums, and the kernel's static arrays beside them: every
+    size up to and above what a launch gets without asking, in a fresh process."""
+    r = subprocess.run([sys.executable, "-c", AROUND_48_KB], cwd=ROOT, capture_output=True, text=True, timeout=300)
+    assert r.returncode == 0 and "all sizes" in r.stdout, r.stdout[-2000:] + r.stderr[-2000:]
