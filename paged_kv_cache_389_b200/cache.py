@@ -86,19 +86,23 @@ class PagedKVCache:
         torch = _torch()
         if self.block_scales:
             with self._on(stream):
-                scales = self.key_scales, self.value_scales
                 if pairs is not None and len(pairs):
                     pairs = torch.as_tensor(pairs, device=self.device)
-                    pa_copy_blocks_scaled(self.key_cache, self.value_cache, *scales, pairs, self.err_flag)
+                    pa_copy_blocks_scaled(self.key_cache, self.value_cache, self.key_scales, self.value_scales, pairs, self.err_flag)
                 if len(slots):
-                    slots = torch.as_tensor(slots, device=self.device)
-                    pa_cache_write_scaled(k, v, slots, self.key_cache, self.value_cache, *scales, self.err_flag)
+                    self._store(k, v, torch.as_tensor(slots, device=self.device))
             return
         if pairs is not None and len(pairs):
             pairs = torch.as_tensor(pairs, device=self.device)
             pa_copy_blocks(self.key_cache, self.value_cache, pairs, self.err_flag, stream)
         if len(slots):
-            slots = torch.as_tensor(slots, device=self.device)
+            self._store(k, v, torch.as_tensor(slots, device=self.device), stream)
+
+    def _store(self, k, v, slots, stream=None):
+        if self.block_scales:
+            pa_cache_write_scaled(k, v, slots, self.key_cache, self.value_cache, self.key_scales, self.value_scales,
+                                  self.err_flag, stream)
+        else:
             pa_cache_write(k, v, slots, self.key_cache, self.value_cache, self.err_flag, stream, self.k_scale, self.v_scale)
 
     def append(self, seqs, k, v, counts=None, stream=None):
@@ -159,14 +163,16 @@ class PagedKVCache:
         if self.dtype == torch.float32:
             raise ValueError("prompt() computes in bf16: a bf16 or 8-bit pool wanted")
         with self._on(stream):
+            # What the append or the attention refuse, they refuse before the manager hands out
+            # blocks: the append is asked first, without tokens.
+            self._store(k[:0], v[:0], torch.empty(0, dtype=torch.int64, device=self.device))
             starts = torch.from_numpy(np.concatenate([[0], np.cumsum(counts)]).astype(np.int32)).to(self.device)
             out = torch.empty(q.shape, dtype=q.dtype, device=self.device) if out is None else out
             ws = self._scratch(pa_prefill_packed_workspace_size(q.shape[0], len(counts), q.shape[1], self.num_kv_heads))
-            # what this refuses, it refuses before the manager hands out blocks
             pa_prefill_packed(q, k, v, starts, max(counts, default=0), scale, out, ws, self.err_flag)
-            slots, pairs = self.plan_append(seqs, counts)
             if not self.block_scales:
                 k, v = k.contiguous(), v.contiguous()
+            slots, pairs = self.plan_append(seqs, counts)
             self.write(k, v, slots, pairs)
         return out
 

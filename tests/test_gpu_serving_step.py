@@ -307,3 +307,30 @@ def test_calls_that_overlap(pa):
         torch.cuda.synchronize()
         assert torch.equal(got[0], want[0]) and torch.equal(got[1], want[1]) and torch.equal(got[2], want[1])
     assert int(err) == 0
+
+
+def test_prompt_refuses_what_the_write_would(pa):
+    """What the append would refuse -- rows of another head_dim or head count than the pool's, a
+    pool it cannot write -- prompt() refuses before the manager hands out blocks."""
+    from paged_kv_cache_389_b200.cache import PagedKVCache
+    torch = torch_mod()
+    rng = np.random.default_rng(2)
+    e4m3 = torch.float8_e4m3fn
+    pools = [PagedKVCache(8, 2, 128, torch.int8, block_scales=True), PagedKVCache(8, 2, 128, e4m3, block_scales=True),
+             PagedKVCache(8, 2, 128, torch.bfloat16), PagedKVCache(8, 2, 128, e4m3),
+             PagedKVCache(8, 2, 64, e4m3),                       # one scale: written at head_dim 128 only
+             PagedKVCache(8, 2, 128, e4m3, k_scale=0.0)]
+    wrong = [[(4, 2, 64), (4, 1, 128), (4, 4, 128)]] * 4 + [[(4, 2, 64)], [(4, 2, 128)]]
+    for kv, shapes in zip(pools, wrong):
+        kv.add_seq(0)
+        for hq, hkv, d in shapes:
+            q, k, v = rows(rng, 40, hq + 2 * hkv, d).split([hq, hkv, hkv], 1)
+            with pytest.raises((ValueError, AssertionError, pa.PAError)):
+                kv.prompt(q, k, v, [0], [40], 0.1)
+            assert kv.manager.num_tokens(0) == 0 and kv.manager.num_free() == 8
+    for kv in pools[:4]:                                         # and is none the worse for it
+        q, k, v = rows(rng, 40, 8, 128).split([4, 2, 2], 1)
+        out = kv.prompt(q, k, v, [0], [40], 0.1)
+        o, mass, reach = step_ops.packed_attention(f64(q), f64(k), f64(v), np.array([0, 40]), 0.1)
+        within(f64(out), o, mass, reach, (0, 2.0 ** -8, 0.0))
+        assert kv.manager.num_tokens(0) == 40 and pa.pa_wait(kv.err_flag) == 0
