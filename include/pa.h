@@ -358,7 +358,8 @@ PA_API pa_status pa_step_plan(const int32_t *counts, const int32_t *context_lens
  * new_context_lens[s] = 0; the other sequences keep theirs.  In place as above; all
  * or nothing (PA_DEVERR_PLAN) when a length does not fit its table or the stack its
  * capacity.  A block must be in one table only: blocks shared by a fork belong to
- * the host manager.
+ * the host manager.  Ids are pushed as they stand; a negative one within a length sets
+ * PA_DEVERR_BLOCK_ID too.
  */
 PA_API pa_status pa_step_release(const int32_t *finished, const int32_t *context_lens, int32_t num_seqs,
                                  int32_t *block_tables, int32_t max_blocks_per_seq, int32_t *free_blocks,

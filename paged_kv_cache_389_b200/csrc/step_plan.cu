@@ -158,7 +158,9 @@ __global__ void __launch_bounds__(kPlanThreads, 1) step_plan_kernel(const StepPl
         for (int j = tid; j < (int)blocks; j += nthreads) {
             const int s = find_seq(pops, S, j);
             int32_t *entry = p.tables + (int64_t)s * p.max_blocks + (j - pops[s]);
-            p.free_out[nfree + j] = *entry;
+            const int32_t id = *entry;
+            if (id < 0) flag_error(p.err, PA_DEVERR_BLOCK_ID);
+            p.free_out[nfree + j] = id;
             *entry = -1;
         }
         return;

@@ -322,3 +322,28 @@ def test_sizes_around_48_kb_of_shared_memory(pa):
     size up to and above what a launch gets without asking, in a fresh process."""
     r = subprocess.run([sys.executable, "-c", AROUND_48_KB], cwd=ROOT, capture_output=True, text=True, timeout=300)
     assert r.returncode == 0 and "all sizes" in r.stdout, r.stdout[-2000:] + r.stderr[-2000:]
+
+
+@pytest.mark.gpu
+@pytest.mark.parametrize("S", [3, 2500])
+def test_release_of_a_negative_table_entry_is_flagged(pa, S):
+    """A negative id within a finished sequence's length: flagged, as the plan flags it."""
+    torch = torch_mod()
+    tables = np.arange(2 * S, dtype=np.int32).reshape(S, 2)
+    tables[0, 1] = -4                     # inside the length
+    tables[1, 1] = -4                     # behind it
+    tables[2] = -4                        # of a sequence that goes on
+    lens, fin = np.full(S, 20, np.int32), np.ones(S, np.int32)
+    lens[1], fin[2] = 16, 0
+    td, nf, err = dev(tables), dev(np.zeros(1, np.int32)), dev(np.zeros(1, np.int32))
+    free, ld = torch.full((2 * S,), 77, dtype=torch.int32, device="cuda"), dev(lens)
+    pa.pa_step_release(dev(fin), ld, td, free, nf, err_flag=err)
+    assert pa.pa_wait(err) == pa.PA_DEVERR_BLOCK_ID
+    want = [int(b) for s in range(S) if fin[s] for b in tables[s, :-(-lens[s] // 16)]]
+    assert free[:int(nf)].tolist() == want and (free[int(nf):] == 77).all()
+    assert ld.tolist() == [20 if s == 2 else 0 for s in range(S)]
+    tables[0, 1] = 1                      # the same without it: no flag
+    td, nf, ld = dev(tables), dev(np.zeros(1, np.int32)), dev(lens)
+    err.zero_()
+    pa.pa_step_release(dev(fin), ld, td, free, nf, err_flag=err)
+    assert pa.pa_wait(err) == 0
