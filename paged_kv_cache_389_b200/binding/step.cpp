@@ -136,7 +136,9 @@ struct Workspace {
     }
 };
 
-// Makes `dev` the current device for the call and gives the stream to launch on.
+// Makes `dev` the current device for the call and gives the stream to launch on.  While it lives
+// the interpreter lock is free, as ctypes leaves it for the library's other calls: a launch that
+// waits for room in a full queue does not hold up the program's other threads.
 class Launch {
 public:
     Launch(int dev, PyObject *stream) {
@@ -151,12 +153,17 @@ public:
             if (PyErr_Occurred()) throw Refused{nullptr, {}};
         }
         guard_.set_index((c10::DeviceIndex)dev);
+        state_ = PyEval_SaveThread();
     }
+    ~Launch() { PyEval_RestoreThread(state_); }
+    Launch(const Launch &) = delete;
+    Launch &operator=(const Launch &) = delete;
     void *stream() const { return s_; }
 
 private:
     c10::cuda::OptionalCUDAGuard guard_;
     void *s_;
+    PyThreadState *state_;
 };
 
 using Args = PyObject *const *;

@@ -347,3 +347,40 @@ def test_release_of_a_negative_table_entry_is_flagged(pa, S):
     err.zero_()
     pa.pa_step_release(dev(fin), ld, td, free, nf, err_flag=err)
     assert pa.pa_wait(err) == 0
+
+
+@pytest.mark.gpu
+def test_other_threads_run_while_a_call_waits(pa):
+    """The launch queue holds about a thousand launches; a call behind a full one waits for room,
+    and the program's other threads run meanwhile."""
+    torch = torch_mod()
+    counts, lens, tables, free, nf, cap = case(np.random.default_rng(0), 4, 1, 40)
+    t = [dev(x) for x in (counts * 0, lens, tables, free, np.array([nf], np.int32))]
+    slots, starts = torch.zeros(cap, dtype=torch.int64, device="cuda"), torch.zeros(5, dtype=torch.int32, device="cuda")
+    err = torch.zeros(1, dtype=torch.int32, device="cuda")
+    pa.pa_step_plan(*t, slots, starts, err_flag=err)
+    torch.cuda.synchronize()
+    beats, stop = [], threading.Event()
+
+    def beat():
+        while not stop.is_set():
+            beats.append(time.monotonic())
+            time.sleep(0.002)
+
+    thread = threading.Thread(target=beat)
+    thread.start()
+    try:
+        begin = time.monotonic()
+        torch.cuda._sleep(2 * 10 ** 9)             # about a second
+        for _ in range(3000):
+            pa.pa_step_plan(*t, slots, starts, err_flag=err)
+        issued = time.monotonic()
+    finally:
+        stop.set()
+        thread.join()
+    torch.cuda.synchronize()
+    assert issued - begin > 0.5, "the queue did not fill: the test says nothing"
+    # a thread that waits for the interpreter gets it within milliseconds; one that cannot have it waits
+    # out the sleeping kernel
+    assert max(b - a for a, b in zip(beats, beats[1:])) < 0.25
+    assert int(err) == 0
