@@ -10,6 +10,8 @@ from __future__ import annotations
 
 import concurrent.futures as cf
 import glob
+import importlib.metadata
+import importlib.util
 import os
 import subprocess
 import sys
@@ -59,14 +61,37 @@ def _compile(src: str, extra: list[str]) -> str:
     return obj
 
 
-def build_binding(force: bool = False) -> str:
-    """Compile the binding of the serving-step calls, linked to the library beside it."""
+def _made_for() -> str | None:
+    """What the binding is compiled against: Python and torch.  None where there is no torch."""
+    if importlib.util.find_spec("torch") is None:
+        return None
+    try:
+        version = importlib.metadata.version("torch")
+    except importlib.metadata.PackageNotFoundError:
+        import torch
+        version = torch.__version__
+    return f"{sys.implementation.cache_tag} torch {version}"
+
+
+def build_binding(force: bool = False) -> str | None:
+    """Compile the binding of the serving-step calls, linked to the library beside it.  It is
+    compiled again when its source, Python or torch has changed.  Without torch (or with one
+    without CUDA) there is nothing that could call it: the library is built alone, and None returned."""
+    made_for, stamp = _made_for(), os.path.join(OBJ, "step.made_for")
+    if made_for is None:
+        print("no torch: the binding of the serving-step calls is left out", file=sys.stderr)
+        return None
     inputs = [BINDING, os.path.join(INCLUDE, "pa.h"), __file__]
     if not force and os.path.exists(STEP) and all(os.path.getmtime(f) <= os.path.getmtime(STEP) for f in inputs):
-        return STEP
+        if os.path.exists(stamp) and open(stamp).read() == made_for:
+            return STEP
     import sysconfig
     import torch
     from torch.utils import cpp_extension
+    if torch.version.cuda is None:
+        print("torch without CUDA: the binding of the serving-step calls is left out", file=sys.stderr)
+        return None
+    os.makedirs(OBJ, exist_ok=True)
     tmp = STEP + f".tmp{os.getpid()}"
     dirs = [INCLUDE] + cpp_extension.include_paths() + [os.path.join(os.path.dirname(os.path.dirname(NVCC)), "include"),
                                                         sysconfig.get_paths()["include"]]
@@ -79,6 +104,8 @@ def build_binding(force: bool = False) -> str:
     if r.returncode != 0:
         raise RuntimeError(f"compile failed: {' '.join(cmd)}\n{r.stdout}\n{r.stderr}")
     os.replace(tmp, STEP)
+    with open(stamp, "w") as f:
+        f.write(made_for)
     return STEP
 
 
