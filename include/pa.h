@@ -413,8 +413,8 @@ PA_API size_t pa_decode_scaled_workspace_size(int32_t num_q_heads, int32_t num_k
  * pa_decode over such pools: one query token per sequence,
  *   out[s][h][:] = sum_t softmax_t(scale * <query[s][h], K_s[t]>) V_s[t],
  * K_s[t] = key code * key_scales[block][kv head] (V alike).  Arguments and errors as in
- * pa_decode; L_s == 0 gives 0.  The scales of blocks in use are finite and not
- * negative (as the append leaves them).  The context is always split evenly over the
+ * pa_decode; L_s == 0 gives 0.  The scales of blocks in use are not negative and at most
+ * 2^122 (the append leaves 2^-64 to 2^122).  The context is always split evenly over the
  * GPU; a sequence's result does not depend on the other sequences beyond the order of fp32
  * sums.  Two kernels (one where max_context_len < 512).  The workspace's contents need
  * not be set and mean nothing afterwards; calls that overlap on the GPU need workspaces of their own.  Replays

@@ -90,6 +90,24 @@ def decode_scaled(q, kpool, vpool, kscales, vscales, tables, lens, scale):
     return out, mass, reach
 
 
+def largest_weight(q, kpool, kscales, vscales, tables, lens, scale):
+    """[S, Hq, 1]: the largest p_t * value scale over a row's tokens, p being the probabilities of
+    decode_scaled -- what its 16-bit weights are relative to."""
+    S, hq, _ = q.shape
+    g = hq // kpool.shape[1]
+    top = np.zeros((S, hq, 1))
+    for s in range(S):
+        n = int(lens[s])
+        blocks = [int(b) for b in tables[s][:-(-n // BLOCK)]]
+        for j in range(hq if n > 0 else 0):
+            h = j // g
+            k = np.concatenate([kpool[b, h] * float(kscales[b, h]) for b in blocks])[:n]
+            x = scale * (k @ q[s, j])
+            p = np.exp(x - x.max())
+            top[s, j] = (p / p.sum() * np.repeat([float(vscales[b, h]) for b in blocks], BLOCK)[:n]).max()
+    return top
+
+
 def packed_attention(q, k, v, starts, scale):
     """Causal attention of every packed sequence; rows outside them are NaN."""
     T, hq, d = q.shape

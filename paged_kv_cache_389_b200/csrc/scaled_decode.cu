@@ -10,7 +10,8 @@
 // far larger or smaller than the others' neither overflows nor loses bits in the
 // 16-bit operands of the tensor cores.  out = O / l * 2^(mo - m).  Both points move
 // only when a p or a w passes 2^8 (a vote per block), so the reductions over lanes
-// are rare.  Sums, maxima and O are fp32; p, w are rounded to f16 (relative 2^-11) for
+// are rare.  Where sigma_v 2^(m - mo) is so large that a p of zero may belong to a w that is
+// not, w is computed as 2^(s + log2(sigma_v) - mo) instead.  Sums, maxima and O are fp32; p, w are rounded to f16 (relative 2^-11) for
 // the product with V; codes are exact in f16; the query is scaled per head by a power
 // of two into the middle of f16's range, which keeps every bf16 bit of its elements down
 // to 2^-24 of the head's largest (smaller ones are off by at most 2^-32 of it).
@@ -58,6 +59,7 @@ constexpr float kLog2e = 1.4426950408889634f;
 constexpr int kWarps = 12;
 constexpr int kThreads = kWarps * 32;
 constexpr float kLazy = 256.f;        // p and w may grow to 2^8 before the reference points move
+constexpr float kFactor = 0x1p100f;   // p below 2^-126 is zero: with a factor up to this, so is its w for f16
 constexpr int kMaxCum = 8192;         // prefix-sum entries in shared memory (every k-th sequence beyond)
 constexpr int kWholeItems = 33;       // longest segments that stay within a CTA
 constexpr int kMergeThreads = 256;
@@ -230,23 +232,26 @@ __device__ __forceinline__ void block_step(unsigned char *stage, const float2 sc
         if (g >= ntok) s[0] = n0, s[1] = n1;
         if (g + 8 >= ntok) s[2] = n0, s[3] = n1;
     }
-    auto weights = [&]() -> bool {
-        const float f0 = sc.y * st.gf[0], f1 = sc.y * st.gf[1];
+    auto probabilities = [&]() {
 #pragma unroll
         for (int i = 0; i < 4; ++i) pr[i] = fast_exp2(fmaf(s[i], i & 1 ? c1 : c0, -st.m[i & 1]));
         if constexpr (kTail) {   // a factor of zero would make the masked ones NaN
             if (g >= ntok) pr[0] = pr[1] = 0.f;
             if (g + 8 >= ntok) pr[2] = pr[3] = 0.f;
         }
-        w[0] = pr[0] * f0;
-        w[1] = pr[1] * f1;
-        w[2] = pr[2] * f0;
-        w[3] = pr[3] * f1;
-        const float a = fmax3(fmax3(pr[0], pr[1], pr[2]), pr[3], w[0]);
-        return fmax3(fmax3(a, w[1], w[2]), w[3], 0.f) <= kLazy;
     };
+    probabilities();
+    const float f0 = sc.y * st.gf[0], f1 = sc.y * st.gf[1];
+    w[0] = pr[0] * f0;
+    w[1] = pr[1] * f1;
+    w[2] = pr[2] * f0;
+    w[3] = pr[3] * f1;
+    // Where the factor is above 2^kFactor (block scales that far apart), a p of zero may stand for a w
+    // that is not: those blocks take the branch below, where w has an exponential of its own.
+    const float a = fmax3(fmax3(pr[0], pr[1], pr[2]), pr[3], w[0]);
+    const float b = fmax3(w[1], w[2], w[3]);
     // m is -inf until the first block: the exponentials are then infinite or NaN
-    const bool fine = weights() && st.m[0] != -INFINITY;
+    const bool fine = fmax3(a, b, fmaxf(f0, f1) * (kLazy / kFactor)) <= kLazy && st.m[0] != -INFINITY;
     if (!__all_sync(kFull, fine)) {
         // move the reference points: the largest score so far, and the largest score plus log2(sigma_v)
         float x0 = -INFINITY, x1 = -INFINITY;
@@ -263,7 +268,7 @@ __device__ __forceinline__ void block_step(unsigned char *stage, const float2 sc
             x0 = fmaxf(x0, __shfl_xor_sync(kFull, x0, off));
             x1 = fmaxf(x1, __shfl_xor_sync(kFull, x1, off));
         }
-        const float lv = fmaxf(__log2f(sc.y), -126.f);
+        const float log_v = __log2f(sc.y), lv = fmaxf(log_v, -100.f);   // m - mo stays within 2^107
         const float x[2] = {x0, x1};
         float ao[2];
 #pragma unroll
@@ -284,7 +289,14 @@ __device__ __forceinline__ void block_step(unsigned char *stage, const float2 sc
             st.o[mt][2] *= ao[0];
             st.o[mt][3] *= ao[1];
         }
-        weights();
+        probabilities();
+        const float v0 = log_v - st.mo[0], v1 = log_v - st.mo[1];
+#pragma unroll
+        for (int i = 0; i < 4; ++i) w[i] = fast_exp2(fmaf(s[i], i & 1 ? c1 : c0, i & 1 ? v1 : v0));
+        if constexpr (kTail) {
+            if (g >= ntok) w[0] = w[1] = 0.f;
+            if (g + 8 >= ntok) w[2] = w[3] = 0.f;
+        }
     }
     st.l[0] += pr[0] + pr[2];
     st.l[1] += pr[1] + pr[3];

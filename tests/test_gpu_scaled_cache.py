@@ -516,3 +516,45 @@ def test_a_context_of_2_31_tokens(pa):
     tol = 2 * (n / 1776) * 2.0 ** -24 + 2.0 ** -11 + 2.0 ** -8 + 2.0 ** -10
     far = np.abs(out.double().cpu().numpy()[0] - w @ v) - tol * (w @ np.abs(v))
     assert (far <= 0).all()
+
+
+@pytest.mark.gpu
+@pytest.mark.parametrize("code", CODES)
+@pytest.mark.parametrize("d", [64, 128])
+@pytest.mark.parametrize("low", [-200, -140, -125, -100, -60])
+def test_decode_value_scales_at_both_ends_of_their_range(pa, code, d, low):
+    """A block of zeros (its scale is the smallest, 2^-64) with one head's largest scores, and a
+    block of values near 2^100 that the head gives 2^low of them and the other heads most: as
+    the append leaves both."""
+    torch = torch_mod()
+    hkv, nb, L = 1, 4, 40
+    q = torch.zeros(1, 4, d, dtype=torch.bfloat16)
+    for h in range(4):
+        q[0, h, h] = 1.0
+    k = np.zeros((L, hkv, d))
+    # natural units: a difference of `low` powers of two
+    k[16:32, 0, 0] = np.round(low * np.log(2))
+    k[16:32, 0, 1] = 40.0
+    v = np.zeros((L, hkv, d))
+    rng = np.random.default_rng(-low)
+    v[16:32] = rng.standard_normal((16, hkv, d)) * 2.0 ** 100
+    kb, vb = bf16(k), bf16(v)
+    slots = np.array([2, 0, 3])[np.arange(L) // 16] * 16 + np.arange(L) % 16
+    kp = np.zeros((nb, hkv, 16, d))
+    sc = np.full((nb, hkv), np.nan, np.float32)
+    got, flag = check_write(pa, kb, vb, slots, kp, kp, sc, sc, code)
+    assert flag == 0 and got[3][2, 0] == 2.0 ** -64 and got[3][0, 0] > 2.0 ** 90
+    tables, lens = np.array([[2, 0, 3]], np.int32), np.array([L], np.int32)
+    S = 3000         # the same sequence over and over: a warp has several blocks in a row
+    c = lambda a: torch.from_numpy(a).cuda()
+    out, err = torch.empty(S, 4, d, dtype=torch.bfloat16, device="cuda"), torch.zeros(1, dtype=torch.int32, device="cuda")
+    ws = torch.empty(pa.pa_decode_scaled_workspace_size(4, 1, d), dtype=torch.uint8, device="cuda")
+    pa.pa_decode_scaled(c(q.float().numpy().repeat(S, 0)).to(torch.bfloat16), to_pool(got[0], code), to_pool(got[1], code), c(got[2]),
+                        c(got[3]), c(tables.repeat(S, 0)), c(lens.repeat(S)), 48, 1.0, out, ws, err)
+    assert pa.pa_wait(err) == 0
+    qq = q.double().numpy()
+    ref, mass, reach = step_ops.decode_scaled(qq, *got, tables, lens, 1.0)
+    top = step_ops.largest_weight(qq, got[0], got[2], got[3], tables, lens, 1.0)
+    bound = step_ops.attention_bound(ref, mass, reach, (0, 2.0 ** -11, 0.0)) + L * 2.0 ** -25 * top * step_ops.TOP[code]
+    g = out.double().cpu().numpy()
+    assert np.isfinite(g).all() and (np.abs(g - ref) <= bound).all()
