@@ -415,13 +415,15 @@ PA_API size_t pa_decode_scaled_workspace_size(int32_t num_q_heads, int32_t num_k
  * K_s[t] = key code * key_scales[block][kv head] (V alike).  Arguments and errors as in
  * pa_decode; L_s == 0 gives 0.  The scales of blocks in use are not negative and at most
  * 2^122 (the append leaves 2^-64 to 2^122).  The context is always split evenly over the
- * GPU; a sequence's result does not depend on the other sequences beyond the order of fp32
- * sums.  Two kernels (one where max_context_len < 512).  The workspace's contents need
- * not be set and mean nothing afterwards; calls that overlap on the GPU need workspaces of their own.  Replays
- * correctly from a graph, following context_lens.  num_seqs <= 16384 and
+ * GPU; where it is cut depends on the other sequences' lengths, so in another batch a result may
+ * differ by rounding (the order of the fp32 sums, and the 16-bit weights below).  Two kernels (one
+ * where max_context_len < 512).  The workspace's contents need not be set and mean nothing
+ * afterwards; calls that overlap on the GPU need workspaces of their own.  Replays correctly
+ * from a graph, following context_lens.  num_seqs <= 16384 and
  * num_seqs * (max_context_len / 16 + 2) < 2^31.  Scores, sums and the accumulator are fp32;
- * probabilities are rounded to f16 for the product with V; the query is exact (elements
- * below 2^-24 of their head's largest: to 2^-32 of it).
+ * probabilities times value scales are rounded to f16 for the product with V (2^-11 of each, or 2^-32
+ * of the row's largest where that is more); the query is exact (elements below 2^-24 of
+ * their head's largest: to 2^-32 of it).
  */
 PA_API pa_status pa_decode_scaled(const void *query, const void *key_cache, const void *value_cache,
                                   const float *key_scales, const float *value_scales,

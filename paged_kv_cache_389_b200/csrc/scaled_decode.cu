@@ -6,15 +6,16 @@
 //   out = sum_t softmax_t(s) sigma_v(b, h) vcode_t
 // online, in units of log2: with a reference point m of the scores and a second one,
 // mo, of the scores plus log2(sigma_v), each token adds p = 2^(s - m) to l and
-// w = p * sigma_v * 2^(m - mo) times its codes to O, so that a block whose values are
-// far larger or smaller than the others' neither overflows nor loses bits in the
-// 16-bit operands of the tensor cores.  out = O / l * 2^(mo - m).  Both points move
-// only when a p or a w passes 2^8 (a vote per block), so the reductions over lanes
-// are rare.  Where sigma_v 2^(m - mo) is so large that a p of zero may belong to a w that is
-// not, w is computed as 2^(s + log2(sigma_v) - mo) instead.  Sums, maxima and O are fp32; p, w are rounded to f16 (relative 2^-11) for
-// the product with V; codes are exact in f16; the query is scaled per head by a power
-// of two into the middle of f16's range, which keeps every bf16 bit of its elements down
-// to 2^-24 of the head's largest (smaller ones are off by at most 2^-32 of it).
+// w = p * sigma_v * 2^(m - mo) times its codes to O, so that the size of a block's values
+// neither overflows the 16-bit operands of the tensor cores nor costs it bits: what counts is
+// w beside the row's largest.  out = O / l * 2^(mo - m).  Both points move only when a p or a
+// w has grown by 2^8 (a vote per block), so the reductions over lanes are rare.
+// Where sigma_v 2^(m - mo) is so large that a p of zero may belong to a w that is
+// not, w is computed as 2^(s + log2(sigma_v) - mo) instead.  Sums, maxima and O are fp32; w is
+// rounded to f16 for the product with V (relative 2^-11; a w below 2^-21 of the row's
+// largest is off by up to 2^-32 of that one); codes are exact in f16; the query is scaled per
+// head by a power of two into the middle of f16's range, which keeps every bf16 bit of its elements
+// down to 2^-24 of the head's largest (smaller ones are off by at most 2^-32 of it).
 //
 // What bounds it: HBM, 2 * L * Hkv * d bytes (in a graph: 256 lognormal contexts, 32/8 heads, e4m3, 1.08
 // GB: 190 us, 5.7 TB/s; 64 contexts, 32/32 heads, int8, 0.58 GB: 102 us; 8 x 32768 tokens, 64/8
@@ -58,7 +59,10 @@ constexpr unsigned kFull = 0xffffffffu;
 constexpr float kLog2e = 1.4426950408889634f;
 constexpr int kWarps = 12;
 constexpr int kThreads = kWarps * 32;
-constexpr float kLazy = 256.f;        // p and w may grow to 2^8 before the reference points move
+// The reference points lie 2^kHead below the largest p and w when they move, and move again when one has
+// grown by 2^8: p and w reach 2^15, inside f16's range, and w loses bits (below f16's normal numbers, 2^-14)
+// only where it is less than 2^-21 of the row's largest.
+constexpr float kHead = 7.f, kLazy = 32768.f;
 constexpr float kFactor = 0x1p100f;   // p below 2^-126 is zero: with a factor up to this, so is its w for f16
 constexpr int kMaxCum = 8192;         // prefix-sum entries in shared memory (every k-th sequence beyond)
 constexpr int kWholeItems = 33;       // longest segments that stay within a CTA
@@ -273,7 +277,7 @@ __device__ __forceinline__ void block_step(unsigned char *stage, const float2 sc
         float ao[2];
 #pragma unroll
         for (int k = 0; k < 2; ++k) {
-            const float m = fmaxf(st.m[k], x[k]), mo = fmaxf(st.mo[k], x[k] + lv);
+            const float m = fmaxf(st.m[k], x[k] - kHead), mo = fmaxf(st.mo[k], x[k] + lv - kHead);
             const float al = st.m[k] == -INFINITY ? 0.f : fast_exp2(st.m[k] - m);
             ao[k] = st.mo[k] == -INFINITY ? 0.f : fast_exp2(st.mo[k] - mo);
             // no finite score yet: any finite reference will do

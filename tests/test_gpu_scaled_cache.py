@@ -518,6 +518,45 @@ def test_a_context_of_2_31_tokens(pa):
     assert (far <= 0).all()
 
 
+def tight_bound(t, ref, mass, reach, lost):
+    """attention_bound, with `lost` of the row's largest weight p * value scale for each 16-bit weight
+    below f16's normal numbers, times the largest code."""
+    top = step_ops.largest_weight(t.q.double().numpy(), t.kp, t.ks, t.vs, t.tables, t.lens, t.scale)
+    return (step_ops.attention_bound(ref, mass, reach, (0, 2.0 ** -11, 0.0))
+            + t.lens[:, None, None] * lost * top * step_ops.TOP[t.code])
+
+
+@pytest.mark.gpu
+@pytest.mark.parametrize("code", CODES)
+@pytest.mark.parametrize("d", [64, 128])
+@pytest.mark.parametrize("reach_down", [13, 16])
+def test_decode_behind_a_key_that_outweighs_the_others(pa, code, d, reach_down):
+    """One token has nearly all of the probability and a value of zero, under the same scale as
+    the others' values: the row is what the other tokens add, 2^-18 to 2^-23 of that weight."""
+    torch = torch_mod()
+    rng = np.random.default_rng(reach_down)
+    t = Decode(pa, code, 8, 2, d, [16, 32, 5, 250], seed=3)
+    t.ks[:], t.vs[:], t.scale = 1.0, 0.5, 1.0
+    t.kp[:] = np.where(np.isnan(t.kp), t.kp, 0.0)
+    first = [int(b) for b in t.tables[:, 0]]
+    for s, n in enumerate(t.lens):
+        for j, b in enumerate(int(b) for b in t.tables[s][:-(-int(n) // 16)]):
+            t.kp[b, :, :, 0] = -rng.integers(reach_down - 1, reach_down + 1, t.kp[b, :, :, 0].shape)
+    t.kp[first, :, 0, 0] = 0.0
+    t.vp[first, :, 0] = 0.0
+    t.q[:] = 0.0
+    t.q[..., 0] = 1.0
+    c = lambda a: torch.from_numpy(a).cuda()
+    t.t[:4] = [to_pool(t.kp, code), to_pool(t.vp, code), c(t.ks), c(t.vs)]
+    t.qd = t.q.cuda()
+    t.call()
+    assert pa.pa_wait(t.err) == 0
+    ref, mass, reach = step_ops.decode_scaled(t.q.double().numpy(), t.kp, t.vp, t.ks, t.vs, t.tables, t.lens, t.scale)
+    got = t.out.double().cpu().numpy()
+    # weights are kept to 2^-11, and below 2^-21 of the largest one to 2^-32 of it
+    assert np.isfinite(got).all() and (np.abs(got - ref) <= tight_bound(t, ref, mass, reach, 2.0 ** -32)).all()
+
+
 @pytest.mark.gpu
 @pytest.mark.parametrize("code", CODES)
 @pytest.mark.parametrize("d", [64, 128])
