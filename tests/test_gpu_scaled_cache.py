@@ -529,6 +529,29 @@ def tight_bound(t, ref, mass, reach, lost):
 @pytest.mark.gpu
 @pytest.mark.parametrize("code", CODES)
 @pytest.mark.parametrize("d", [64, 128])
+def test_decode_blocks_of_very_different_size_closely(pa, code, d):
+    """Scales far apart within a sequence, within what 16-bit weights lose: 2^-25 of the
+    row's largest weight each (f16's smallest step is 2^-24, and no reference point lies above
+    the largest weight)."""
+    torch = torch_mod()
+    rng = np.random.default_rng(1)
+    t = Decode(pa, code, 8, 2, d, [400, 37, 1200], seed=9, spread=0.5)
+    live = ~np.isnan(t.ks)
+    for s, lo, hi in ((t.vs, -40, 40), (t.ks, -30, 2)):
+        s[live] *= 2.0 ** rng.integers(lo, hi, live.sum())
+    t.t[2], t.t[3] = torch.from_numpy(t.ks).cuda(), torch.from_numpy(t.vs).cuda()
+    t.call()
+    assert pa.pa_wait(t.err) == 0
+    ref, mass, reach = step_ops.decode_scaled(t.q.double().numpy(), t.kp, t.vp, t.ks, t.vs, t.tables, t.lens, t.scale)
+    got, bound = t.out.double().cpu().numpy(), tight_bound(t, ref, mass, reach, 2.0 ** -25)
+    assert np.isfinite(got).all() and (np.abs(got - ref) <= bound).all()
+    # the bound is tight enough to see two percent, in every sequence
+    assert (np.abs(1.02 * ref - ref) > bound).any((1, 2)).all()
+
+
+@pytest.mark.gpu
+@pytest.mark.parametrize("code", CODES)
+@pytest.mark.parametrize("d", [64, 128])
 @pytest.mark.parametrize("reach_down", [13, 16])
 def test_decode_behind_a_key_that_outweighs_the_others(pa, code, d, reach_down):
     """One token has nearly all of the probability and a value of zero, under the same scale as
