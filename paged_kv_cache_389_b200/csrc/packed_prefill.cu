@@ -50,7 +50,7 @@
 // anything.  Its value meets P = 0 in the tensor core, where an infinity or a NaN would
 // survive: the loader zeroes the rows of the last tile that no row of the job sees, and a
 // row that comes out not finite while a value masked for it is not finite is
-// computed again without tensor cores (redo_row).
+// computed again (redo_rows).
 // Every wait is bounded; an abort drains the copies and MMAs in flight and frees the
 // tensor memory.
 #include <cuda.h>
@@ -122,6 +122,12 @@ enum Bar {
     kNumBars = kBarRead + kJobSlots
 };
 
+struct Misc {                     // in shared memory
+    uint32_t tmem;                // tensor-memory address
+    int abort;                    // raised by the first warp whose wait ran out
+    unsigned long long step;      // when redo_rows took its last step
+};
+
 template <int D>
 struct Smem {
     static constexpr int kHalves = D / 64;
@@ -133,8 +139,8 @@ struct Smem {
     static constexpr uint32_t kV = kK + kStages * kTileBytes;
     static constexpr uint32_t kOut = kV + kStages * kTileBytes;
     static constexpr uint32_t kBars = kOut + 8 * kOutBytes;
-    static constexpr uint32_t kMisc = kBars + kNumBars * 8;              // tensor-memory address, abort flag
-    static constexpr uint32_t kJobs = (kMisc + 8 + 15) / 16 * 16;        // int4 [8] records, int [8] tags
+    static constexpr uint32_t kMisc = kBars + kNumBars * 8;              // Misc
+    static constexpr uint32_t kJobs = (kMisc + sizeof(Misc) + 15) / 16 * 16;     // int4 [8] records, int [8] tags
     static constexpr size_t kBytes = kJobs + 8 * 16 + 8 * 4 + 1024;      // slack to align the base
     static_assert(kQBytes % 1024 == 0 && kHalf % 1024 == 0 && kBars % 8 == 0, "swizzled tiles 1024-byte aligned");
     static_assert(kBytes <= 232448, "shared memory of an sm_100 CTA");
@@ -263,8 +269,26 @@ __global__ void __launch_bounds__(kPlanThreads, 1) packed_plan_kernel(const Plan
 }
 
 // ---------------------------------------------------------------- the attention
-__device__ __forceinline__ bool wait_bar(uint64_t *bar, uint32_t parity, volatile int *abort, const Params &p) {
-    return mbar_wait_bounded(bar, parity, abort, p.err, p.wait_ns);
+// Within a wait since t0: false when another warp gave up or the bound has passed.  It counts from
+// the last step of redo_rows: that takes as long as its prompt is, and is no wait that ran out.
+__device__ __forceinline__ bool may_wait(unsigned long long t0, volatile Misc *misc, const Params &p) {
+    if (misc->abort) return false;
+    const unsigned long long now = global_ns();
+    if (now - t0 <= p.wait_ns) return true;
+    const unsigned long long step = misc->step;
+    if (step >= now || now - step <= p.wait_ns) return true;
+    misc->abort = 1;
+    flag_error(p.err, PA_DEVERR_TIMEOUT);
+    return false;
+}
+
+__device__ __forceinline__ bool wait_bar(uint64_t *bar, uint32_t parity, volatile Misc *misc, const Params &p) {
+    if (mbar_try_wait(bar, parity)) return true;
+    const unsigned long long t0 = global_ns();
+    for (uint32_t it = 1;; ++it) {
+        if (mbar_try_wait(bar, parity)) return true;
+        if ((it & 7u) == 0 && !may_wait(t0, misc, p)) return false;
+    }
 }
 
 struct Job {
@@ -298,45 +322,131 @@ __device__ __forceinline__ float fmax3(float a, float b, float c) {
     return r;
 }
 
-// One output row (token i of the sequence at row0, query head hq) without tensor cores, by
-// a whole warp: only keys 0 .. i are read, so nothing masked can reach it.
+// The last key of [from, end) whose value holds an infinity or a NaN; -1 if none does.
 template <int D>
-__device__ __noinline__ void redo_row(const Params &p, int row0, int i, int hq, int h, int lane) {
-    constexpr int E = D / 32;
-    const __nv_bfloat16 *q = reinterpret_cast<const __nv_bfloat16 *>(p.q + (int64_t)(row0 + i) * p.q_stride) + hq * D;
-    float qv[E], acc[E], m = -INFINITY, l = 0.f;
-    for (int e = 0; e < E; ++e) {
-        qv[e] = __bfloat162float(q[lane * E + e]);
-        acc[e] = 0.f;
+__device__ __forceinline__ int last_not_finite(const Params &p, int row0, int from, int end, int h, int lane, volatile Misc *misc) {
+    for (int j = end - 1; j >= from; --j) {
+        const uint16_t *v = reinterpret_cast<const uint16_t *>(p.v + (int64_t)(row0 + j) * p.v_stride) + h * D;
+        bool found = false;
+        for (int e = lane; e < D; e += 32) found |= (v[e] & 0x7fffu) >= 0x7f80u;
+        if (__any_sync(kFull, found)) return j;
+        if (lane == 0) misc->step = global_ns();
     }
-    for (int j = 0; j <= i; ++j) {
-        const __nv_bfloat16 *k = reinterpret_cast<const __nv_bfloat16 *>(p.k + (int64_t)(row0 + j) * p.k_stride) + h * D;
-        const __nv_bfloat16 *v = reinterpret_cast<const __nv_bfloat16 *>(p.v + (int64_t)(row0 + j) * p.v_stride) + h * D;
-        float s = 0.f;
-        for (int e = 0; e < E; ++e) s = fmaf(qv[e], __bfloat162float(k[lane * E + e]), s);
-        for (int o = 16; o > 0; o >>= 1) s += __shfl_xor_sync(kFull, s, o);
-        s *= p.scale_log2;
-        const float mn = fmaxf(m, s);
-        const float base = mn == -INFINITY ? 0.f : mn;
-        const float a = exp2f(m - base), w = exp2f(s - base);
-        m = mn;
-        l = l * a + w;
-        for (int e = 0; e < E; ++e) acc[e] = acc[e] * a + w * __bfloat162float(v[lane * E + e]);
-        if (l != l) break;  // a visible score is not a number: so is the row
-    }
-    __nv_bfloat16 *out = reinterpret_cast<__nv_bfloat16 *>(p.out) + ((int64_t)(row0 + i) * p.num_q_heads + hq) * D;
-    for (int e = 0; e < E; ++e) out[lane * E + e] = __float2bfloat16_rn(l != l ? l : l > 0.f ? acc[e] / l : 0.f);
+    return -1;
 }
 
-// Does any value behind token i, up to key `end` of the sequence, hold an infinity or a NaN?
-template <int D>
-__device__ __noinline__ bool masked_not_finite(const Params &p, int row0, int i, int end, int h, int lane) {
-    bool found = false;
-    for (int j = i + 1; j < end; ++j) {
-        const __nv_bfloat16 *v = reinterpret_cast<const __nv_bfloat16 *>(p.v + (int64_t)(row0 + j) * p.v_stride) + h * D;
-        for (int e = lane; e < D; e += 32) found |= !isfinite(__bfloat162float(v[e]));
+// Eight rows of a tile again, those whose bit is set in `want`, by a whole warp: row x is token
+// tok0 + x / G of the sequence at row0, query head h G + x % G.  A value meets only the rows that
+// see it (a row's sum skips the others), so nothing masked can reach one.
+// Scores eight keys at a time on 16 x 8 tiles, whose lower half is empty (lane 4 g + t: row g, dims
+// D / 4 t .. of queries, keys, values and sums, keys 2 t and 2 t + 1 of the scores); the sums in
+// fp32 fused multiply-adds.  A prompt of 16,384 tokens, 32/8 heads, head_dim 128, whose last value
+// is not finite: 37 ms (1.7 without; one row after the other, a key at a time, 307).  Sixteen rows at a
+// time left the softmax warps fewer registers: 24 short prompts 12.4 us instead of 11.6.
+template <int D, int G>
+__device__ __forceinline__ void redo_eight(const Params &p, int row0, int tok0, int h, unsigned want, int lane,
+                                           volatile Misc *misc) {
+    constexpr int E = D / 4;
+    const int g = lane >> 2, t = lane & 3;
+    const int tok = tok0 + g / G, hq = h * G + g % G;
+    const bool mine = (want >> g & 1u) != 0;
+    const int last = tok0 + (31 - __clz(want)) / G;      // the last key that one of the rows sees
+    uint32_t qa[D / 16][2];
+    const unsigned char *qr = p.q + (int64_t)(row0 + tok) * p.q_stride + (hq * D + E * t) * 2;
+#pragma unroll
+    for (int i = 0; i < E / 8; ++i) {
+        uint4 x = make_uint4(0, 0, 0, 0);
+        if (mine) x = __ldg(reinterpret_cast<const uint4 *>(qr) + i);
+        qa[2 * i][0] = x.x;
+        qa[2 * i][1] = x.y;
+        qa[2 * i + 1][0] = x.z;
+        qa[2 * i + 1][1] = x.w;
     }
-    return __any_sync(kFull, found);
+    float acc[E], m = -INFINITY, l = 0.f;
+#pragma unroll
+    for (int e = 0; e < E; ++e) acc[e] = 0.f;
+#pragma unroll 1
+    for (int kb = 0; kb <= last; kb += 8) {
+        const unsigned char *kr = p.k + (int64_t)(row0 + kb + g) * p.k_stride + (h * D + E * t) * 2;
+        float s[4] = {0.f, 0.f, 0.f, 0.f};
+#pragma unroll
+        for (int i = 0; i < E / 8; ++i) {
+            uint4 x = make_uint4(0, 0, 0, 0);
+            if (kb + g <= last) x = __ldg(reinterpret_cast<const uint4 *>(kr) + i);
+            const uint32_t a0[4] = {qa[2 * i][0], 0u, qa[2 * i][1], 0u}, a1[4] = {qa[2 * i + 1][0], 0u, qa[2 * i + 1][1], 0u};
+            mma_bf16_16816(s, a0, x.x, x.y);
+            mma_bf16_16816(s, a1, x.z, x.w);
+        }
+        const bool see0 = kb + 2 * t <= tok, see1 = kb + 2 * t + 1 <= tok;
+        const float s0 = s[0] * p.scale_log2, s1 = s[1] * p.scale_log2;
+        float mn = m;
+        if (see0) mn = fmaxf(mn, s0);
+        if (see1) mn = fmaxf(mn, s1);
+        mn = fmaxf(mn, __shfl_xor_sync(kFull, mn, 1));
+        mn = fmaxf(mn, __shfl_xor_sync(kFull, mn, 2));
+        const float base = mn == -INFINITY ? 0.f : mn, a = exp2f(m - base);
+        m = mn;
+        const float p0 = see0 ? exp2f(s0 - base) : 0.f, p1 = see1 ? exp2f(s1 - base) : 0.f;
+        l = l * a + (p0 + p1);
+        if (a != 1.f) {
+#pragma unroll
+            for (int e = 0; e < E; ++e) acc[e] *= a;
+        }
+        const int keys = min(8, last + 1 - kb);
+#pragma unroll 1
+        for (int c = 0; c < keys; ++c) {
+            const float w = __shfl_sync(kFull, c & 1 ? p1 : p0, (lane & 28) | (c >> 1));
+            const uint4 *vr = reinterpret_cast<const uint4 *>(p.v + (int64_t)(row0 + kb + c) * p.v_stride + (h * D + E * t) * 2);
+            uint4 x[E / 8];
+#pragma unroll
+            for (int i = 0; i < E / 8; ++i) x[i] = __ldg(vr + i);
+            if (kb + c > tok) continue;
+#pragma unroll
+            for (int i = 0; i < E / 8; ++i) {
+                const uint32_t v2[4] = {x[i].x, x[i].y, x[i].z, x[i].w};
+#pragma unroll
+                for (int y = 0; y < 4; ++y) {
+                    const float2 v = __bfloat1622float2(*reinterpret_cast<const __nv_bfloat162 *>(&v2[y]));
+                    acc[8 * i + 2 * y] = fmaf(w, v.x, acc[8 * i + 2 * y]);
+                    acc[8 * i + 2 * y + 1] = fmaf(w, v.y, acc[8 * i + 2 * y + 1]);
+                }
+            }
+        }
+        if (lane == 0) misc->step = global_ns();
+        if ((kb & 127) == 0) {
+            // a sum that is NaN stays NaN: nothing to add where all are
+            bool done = true;
+#pragma unroll
+            for (int e = 0; e < E; ++e) done &= !mine || acc[e] != acc[e];
+            if (__all_sync(kFull, done)) break;
+            if (__any_sync(kFull, misc->abort != 0)) return;
+        }
+    }
+    l += __shfl_xor_sync(kFull, l, 1);
+    l += __shfl_xor_sync(kFull, l, 2);
+    if (!mine) return;
+    uint4 *dst = reinterpret_cast<uint4 *>(p.out + (((int64_t)(row0 + tok) * p.num_q_heads + hq) * D + E * t) * 2);
+    const float f = l > 0.f ? 1.f / l : l;               // NaN stays NaN
+#pragma unroll
+    for (int i = 0; i < E / 8; ++i) {
+        uint32_t w[4];
+#pragma unroll
+        for (int y = 0; y < 4; ++y) w[y] = pack_bf16x2(acc[8 * i + 2 * y] * f, acc[8 * i + 2 * y + 1] * f);
+        dst[i] = make_uint4(w[0], w[1], w[2], w[3]);
+    }
+}
+
+// Of a softmax warp's 32 rows, the first of them token tok0, those whose bit is set in `odd` came out
+// not finite: where a value masked for them is not finite, among the keys below `end` that their
+// tiles held, they are computed again.  (A row that sees the last such value is what it should be.)
+template <int D, int G>
+__device__ __noinline__ void redo_rows(const Params &p, int row0, int tok0, int h, int end, unsigned odd, volatile Misc *misc) {
+    const int lane = threadIdx.x & 31;
+    const int worst = last_not_finite<D>(p, row0, tok0 + 1, end, h, lane, misc);
+    odd &= __ballot_sync(kFull, tok0 + lane / G < worst);
+#pragma unroll 1
+    for (int x = 0; x < 32; x += 8)
+        if (odd >> x & 0xffu) redo_eight<D, G>(p, row0, tok0 + x / G, h, odd >> x & 0xffu, lane, misc);
 }
 
 template <int D, int G>
@@ -350,8 +460,7 @@ __global__ void __launch_bounds__(kThreads, 1) packed_prefill_kernel(const __gri
     unsigned char *smem = smem_raw + ((1024 - (smem_u32(smem_raw) & 1023)) & 1023);
     const uint32_t sbase = smem_u32(smem);
     uint64_t *bars = reinterpret_cast<uint64_t *>(smem + SM::kBars);
-    uint32_t *tmem_slot = reinterpret_cast<uint32_t *>(smem + SM::kMisc);
-    volatile int *abort_flag = reinterpret_cast<volatile int *>(smem + SM::kMisc + 4);
+    volatile Misc *misc = reinterpret_cast<volatile Misc *>(smem + SM::kMisc);
     // The K loader draws the CTA's jobs and publishes job k in slot k & 7 (a record without
     // tokens ends the work); the other warps read it there.
     volatile int *job_rec = reinterpret_cast<volatile int *>(smem + SM::kJobs);
@@ -365,7 +474,8 @@ __global__ void __launch_bounds__(kThreads, 1) packed_prefill_kernel(const __gri
             const bool both = i < kBarVLand || i == kBarQEmpty;
             mbar_init(&bars[i], rows ? 128 : i >= kBarRead ? 8 : both ? 2 : 1);
         }
-        *abort_flag = 0;
+        misc->abort = 0;
+        misc->step = 0;
         mbar_init_fence();
     }
     if (warp == kLoadWarp && lane == 0) {
@@ -373,25 +483,18 @@ __global__ void __launch_bounds__(kThreads, 1) packed_prefill_kernel(const __gri
         tc::prefetch_map(&p.kmap);
         tc::prefetch_map(&p.vmap);
     }
-    if (warp == kMmaWarp) tc::alloc(tmem_slot, TL::kCols);
+    if (warp == kMmaWarp) tc::alloc(const_cast<uint32_t *>(&misc->tmem), TL::kCols);
     tc::fence_before();
     __syncthreads();
     tc::fence_after();
-    const uint32_t tmem = *tmem_slot;
+    const uint32_t tmem = misc->tmem;
 
     auto read_job_warp = [&](int k, Job &jb) -> bool {
         int ok = 0;
         if (lane == 0) {
             const unsigned long long t0 = global_ns();
             ok = 1;
-            while (job_tag[k & 7] != k) {
-                if (*abort_flag || global_ns() - t0 > p.wait_ns) {
-                    if (!*abort_flag) flag_error(p.err, PA_DEVERR_TIMEOUT);
-                    *abort_flag = 1;
-                    ok = 0;
-                    break;
-                }
-            }
+            while (ok && job_tag[k & 7] != k) ok = may_wait(t0, misc, p);
             __threadfence_block();
         }
         ok = __shfl_sync(kFull, ok, 0);
@@ -440,7 +543,7 @@ __global__ void __launch_bounds__(kThreads, 1) packed_prefill_kernel(const __gri
                     }
                     // A stream without rows in a job does not hold the others up, so a softmax warp
                     // may be jobs behind: its record has to stay until it has read it.
-                    if (k >= kJobSlots) ok = wait_bar(&bars[kBarRead + (k & 7)], ((k >> 3) - 1) & 1, abort_flag, p);
+                    if (k >= kJobSlots) ok = wait_bar(&bars[kBarRead + (k & 7)], ((k >> 3) - 1) & 1, misc, p);
                     if (!ok) break;
                     job_rec[(k & 7) * 4] = rec.x;
                     job_rec[(k & 7) * 4 + 1] = rec.y;
@@ -453,7 +556,7 @@ __global__ void __launch_bounds__(kThreads, 1) packed_prefill_kernel(const __gri
                     u = p.starts ? u + (int)gridDim.x : (int)gridDim.x + atomicAdd(p.meta + 1, 1);
                     Job jb;
                     make_job<D, G>(rec, jb);
-                    if (nj > 0) ok = wait_bar(&bars[kBarQEmpty], (nj - 1) & 1, abort_flag, p);
+                    if (nj > 0) ok = wait_bar(&bars[kBarQEmpty], (nj - 1) & 1, misc, p);
                     for (int t = 0; ok && t < 2; ++t) {
                         if (jb.ntiles[t] == 0) continue;
                         mbar_arrive_expect_tx(&bars[kBarQFull + t], SM::kQBytes);
@@ -465,7 +568,7 @@ __global__ void __launch_bounds__(kThreads, 1) packed_prefill_kernel(const __gri
                     const int nt = max(jb.ntiles[0], jb.ntiles[1]);
                     for (int i = 0; ok && i <= nt; ++i, ++it) {
                         const int st = it % kStages;
-                        ok = it < kStages || wait_bar(&bars[kBarEmpty + st], ((it / kStages) - 1) & 1, abort_flag, p);
+                        ok = it < kStages || wait_bar(&bars[kBarEmpty + st], ((it / kStages) - 1) & 1, misc, p);
                         if (!ok) break;
                         if (i == nt) {           // the last slot holds V only
                             mbar_arrive(&bars[kBarFull + st]);
@@ -496,7 +599,7 @@ __global__ void __launch_bounds__(kThreads, 1) packed_prefill_kernel(const __gri
                     const int seen = jb.nkeys - (i - 1) * kKeys;   // rows of V(i - 1) that the job sees
                     const bool tail = i > 0 && seen < kKeys;
                     if (lane == 0) {
-                        ok = it < kStages || wait_bar(&bars[kBarEmpty + st], ((it / kStages) - 1) & 1, abort_flag, p);
+                        ok = it < kStages || wait_bar(&bars[kBarEmpty + st], ((it / kStages) - 1) & 1, misc, p);
                         if (ok && i == 0) mbar_arrive(&bars[kBarFull + st]);   // the first slot holds K only
                         if (ok && i > 0) {
                             uint64_t *bar = tail ? &bars[kBarVLand] : &bars[kBarFull + st];
@@ -505,7 +608,7 @@ __global__ void __launch_bounds__(kThreads, 1) packed_prefill_kernel(const __gri
                                 tc::tma_load_3d(sbase + SM::kV + st * kTileBytes + f * kHalf, &p.vmap, f * 64, jb.h,
                                                 jb.row0 + (i - 1) * kKeys, bar);
                             if (tail) {
-                                ok = wait_bar(bar, nland & 1, abort_flag, p);
+                                ok = wait_bar(bar, nland & 1, misc, p);
                                 if (!ok) mbar_wait_drain(bar, nland & 1);
                             }
                         }
@@ -543,7 +646,7 @@ __global__ void __launch_bounds__(kThreads, 1) packed_prefill_kernel(const __gri
             const uint64_t v_desc = tc::smem_desc(sbase + SM::kV, kHalf, 1024);
             const uint32_t tS = tmem + t * TL::kStream, tP = tS + TL::kP, tO = tS + TL::kO;
             auto wait_all = [&](int bar, uint32_t parity) -> bool {
-                return __all_sync(kFull, wait_bar(&bars[bar], parity, abort_flag, p));
+                return __all_sync(kFull, wait_bar(&bars[bar], parity, misc, p));
             };
             int it = 0;                          // slots of the K/V ring so far
             int nuse = 0, nqk = 0, npv = 0;      // this stream's jobs, QKs and PVs
@@ -601,7 +704,7 @@ __global__ void __launch_bounds__(kThreads, 1) packed_prefill_kernel(const __gri
             if (tc::elect_one()) tc::commit(&bars[kBarIdle + t]);
             __syncwarp();
             if (lane == 0 && !mbar_wait_drain(&bars[kBarIdle + t], 0)) {
-                *abort_flag = 1;
+                misc->abort = 1;
                 flag_error(p.err, PA_DEVERR_TIMEOUT);
             }
             __syncwarp();
@@ -629,7 +732,7 @@ __global__ void __launch_bounds__(kThreads, 1) packed_prefill_kernel(const __gri
             const int lim = row_ok ? tok : INT_MAX;          // padding rows mask nothing
             float m = -INFINITY, l = 0.f;
             for (int j = 0; j < jb.ntiles[t]; ++j) {
-                live = wait_bar(&bars[kBarSFull + t], ns & 1, abort_flag, p);
+                live = wait_bar(&bars[kBarSFull + t], ns & 1, misc, p);
                 live = __all_sync(kFull, live);
                 if (!live) break;
                 tc::fence_after();
@@ -664,7 +767,7 @@ __global__ void __launch_bounds__(kThreads, 1) packed_prefill_kernel(const __gri
                 // P_t may be written, and O_t rescaled, once the stream's last PV is done
                 auto own_p = [&]() {
                     if (ns > 0) {
-                        live = wait_bar(&bars[kBarPFree + t], (ns - 1) & 1, abort_flag, p);
+                        live = wait_bar(&bars[kBarPFree + t], (ns - 1) & 1, misc, p);
                         live = __all_sync(kFull, live);
                         if (!live) return;
                         tc::fence_after();
@@ -714,7 +817,7 @@ __global__ void __launch_bounds__(kThreads, 1) packed_prefill_kernel(const __gri
             }
             if (!live) break;
             // ---- the output rows
-            live = wait_bar(&bars[kBarOFull + t], nuse & 1, abort_flag, p);
+            live = wait_bar(&bars[kBarOFull + t], nuse & 1, misc, p);
             live = __all_sync(kFull, live);
             if (!live) break;
             ++nuse;
@@ -766,14 +869,10 @@ __global__ void __launch_bounds__(kThreads, 1) packed_prefill_kernel(const __gri
                 __syncwarp();
             }
             const bool odd = (bad0.x + bad0.y) + (bad1.x + bad1.y) != 0.f;
-            unsigned again = __ballot_sync(kFull, odd && r < jb.nrows[t]);
-            while (again) {
-                const int ln = __ffs(again) - 1;
-                again &= again - 1;
-                const int rr = qd * 32 + ln, i = jb.i0 + t * kTok + rr / G;
-                if (masked_not_finite<D>(p, jb.row0, i, min(jb.nkeys, jb.ntiles[t] * kKeys), jb.h, lane))
-                    redo_row<D>(p, jb.row0, i, jb.h * G + rr % G, jb.h, lane);
-            }
+            const unsigned again = __ballot_sync(kFull, odd && r < jb.nrows[t]);
+            if (again)
+                redo_rows<D, G>(p, jb.row0, jb.i0 + t * kTok + qd * 32 / G, jb.h, min(jb.nkeys, jb.ntiles[t] * kKeys), again,
+                                misc);
         }
     }
     tc::fence_before();

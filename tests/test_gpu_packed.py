@@ -322,3 +322,71 @@ def test_an_upper_bound_far_above_the_lengths(pa, hq, hkv, d, top):
         out, flag = run(pa, q, k, v, starts, 0.1, top)
         assert flag == 0
         check(out, q, k, v, np.array(starts), 0.1)
+
+
+@pytest.mark.gpu
+@pytest.mark.parametrize("hq,hkv,d", [(2, 1, 128), (4, 4, 128), (8, 2, 64), (16, 2, 128), (4, 2, 64)])
+@pytest.mark.parametrize("scale", [0.1, -0.1])
+def test_rows_between_values_that_are_not_finite(pa, hq, hkv, d, scale):
+    """Infinities that a row sees and a NaN that it does not, in some dims only: its finite dims are the
+    definition's, the others infinite; rows that see the NaN have it in those dims alone."""
+    rng = np.random.default_rng(hq + d)
+    T, at_inf, at_nan = 500, 321, 340
+    q, k, v = inputs(rng, T, hq, hkv, d, False)
+    v[at_inf, :, 3:5] = float("-inf")
+    v[at_nan, :, 4:9] = float("nan")
+    out, flag = run(pa, q, k, v, [0, T], scale)
+    assert flag == 0
+    clean = v.clone()
+    clean[at_inf, :, 3:5], clean[at_nan, :, 4:9] = 0, 0
+    ref, mass, reach = step_ops.packed_attention(*(x.double().cpu().numpy() for x in (q, k, clean)), np.array([0, T]), scale)
+    bound = step_ops.attention_bound(ref, mass, reach, (0, 2.0 ** -8, 0.0))
+    g = out.double().cpu().numpy()
+    isinf, isnan = np.zeros(g.shape, bool), np.zeros(g.shape, bool)
+    isinf[at_inf:, :, 3:5] = True
+    isnan[at_nan:, :, 4:9] = True
+    isinf &= ~isnan
+    assert (g[isinf] == -np.inf).all() and np.isnan(g[isnan]).all()
+    rest = ~isinf & ~isnan
+    assert (np.abs(g - ref) <= bound)[rest].all()
+
+
+@pytest.mark.gpu
+@pytest.mark.parametrize("hq,hkv,d", [(16, 16, 64), (32, 8, 128)])
+def test_rows_computed_again_take_as_long_as_they_take(pa, hq, hkv, d):
+    """The last value of a prompt is not finite: the rows of its tile are computed again over thousands of
+    keys, for longer than the bound of the in-kernel waits, which the CTA's other warps do not take for
+    a wait that ran out; the other rows are what they are without it."""
+    torch = torch_mod()
+    rng = np.random.default_rng(hkv)
+    T = 6144                           # whole pairs of tiles: no stream waits for a whole job of the other
+    q, k, v = inputs(rng, T, hq, hkv, d, False)
+    clean, flag = run(pa, q, k, v, [0, T], 0.1)
+    assert flag == 0
+    v[-1] = float("nan")
+    pa.pa_set_wait_timeout_ns(300_000)
+    try:
+        out, flag = run(pa, q, k, v, [0, T], 0.1)
+    finally:
+        pa.pa_set_wait_timeout_ns(0)
+    assert flag == 0
+    assert torch.isnan(out[-1]).all() and torch.equal(out[:T - 256], clean[:T - 256])
+    f = lambda x: x.double().cpu().numpy()
+    n = 256
+    for h in (0, hq - 1):
+        kk, vv, qq = f(k[:, h // (hq // hkv)]), np.nan_to_num(f(v[:, h // (hq // hkv)])), f(q[T - n:T - 1, h])
+        x = 0.1 * qq @ kk.T
+        dead = np.arange(T)[None, :] > np.arange(T - n, T - 1)[:, None]
+        x[dead] = -np.inf
+        p = np.exp(x - x.max(1, keepdims=True))
+        p /= p.sum(1, keepdims=True)
+        reach = 0.1 * np.where(dead, 0.0, np.abs(qq) @ np.abs(kk).T).max(1, keepdims=True)
+        bound = step_ops.attention_bound(p @ vv, p @ np.abs(vv), reach, (0, 2.0 ** -8, 0.0))
+        assert (np.abs(f(out[T - n:T - 1, h]) - p @ vv) <= bound).all()
+    v[:] = float("nan")
+    pa.pa_set_wait_timeout_ns(300_000)
+    try:
+        out, flag = run(pa, q, k, v, [0, T], 0.1)
+    finally:
+        pa.pa_set_wait_timeout_ns(0)
+    assert flag == 0 and torch.isnan(out).all()
