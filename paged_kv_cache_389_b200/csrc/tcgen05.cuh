@@ -27,11 +27,11 @@ __device__ __forceinline__ bool elect_one() {
     asm volatile("{\n\t.reg .pred q;\n\telect.sync _|q, 0xffffffff;\n\tselp.u32 %0, 1, 0, q;\n\t}" : "=r"(r));
     return r != 0;
 }
-// The three below are executed by a whole converged warp and issued by one elected lane
-// (always the same one).  With the election inside the instruction's own predicate the
-// warp never diverges, so the compiler keeps descriptors in uniform registers: measured on
-// B200, 8 MMAs issued from a lane-0 branch held the warp for 600-800 clocks, longer than the
-// tensor core needs for them.
+// One thread calls the three below: each call is one instruction issued by that thread.  The
+// callers have a whole converged warp branch on elect_one(), so that the same lane issues every
+// time (commit covers what its own thread issued) and the compiler keeps descriptors in uniform
+// registers: measured on B200, 8 MMAs issued from a lane-0 branch held the warp for 600-800
+// clocks, longer than the tensor core needs for them.
 // D (tensor memory) (+)= A (shared-memory descriptor) * B (shared-memory descriptor)
 __device__ __forceinline__ void mma_ss(uint32_t d, uint64_t a_desc, uint64_t b_desc, uint32_t idesc, bool accumulate) {
     asm volatile(
@@ -50,26 +50,13 @@ __device__ __forceinline__ void mma_ts(uint32_t d, uint32_t a, uint64_t b_desc, 
         ::"r"(d), "r"(a), "l"(b_desc), "r"(idesc), "r"(accumulate ? 1u : 0u)
         : "memory");
 }
-// One arrival on `bar` when every tcgen05 operation the elected lane issued so far is done.
+// One arrival on `bar` when every tcgen05 operation this thread issued so far is done.
 __device__ __forceinline__ void commit(uint64_t *bar) {
     asm volatile(
         "tcgen05.commit.cta_group::1.mbarrier::arrive::one.shared::cluster.b64 [%0];" ::"r"(smem_u32(bar))
         : "memory");
 }
-// 32 lanes x 32 columns of 32 bits: thread i gets columns c .. c + 31 of lane base + i
-__device__ __forceinline__ void ld32(uint32_t taddr, float *v) {
-    uint32_t r[32];
-    asm volatile(
-        "tcgen05.ld.sync.aligned.32x32b.x32.b32 {%0,%1,%2,%3,%4,%5,%6,%7,%8,%9,%10,%11,%12,%13,%14,%15,"
-        "%16,%17,%18,%19,%20,%21,%22,%23,%24,%25,%26,%27,%28,%29,%30,%31}, [%32];"
-        : "=r"(r[0]), "=r"(r[1]), "=r"(r[2]), "=r"(r[3]), "=r"(r[4]), "=r"(r[5]), "=r"(r[6]), "=r"(r[7]),
-          "=r"(r[8]), "=r"(r[9]), "=r"(r[10]), "=r"(r[11]), "=r"(r[12]), "=r"(r[13]), "=r"(r[14]), "=r"(r[15]),
-          "=r"(r[16]), "=r"(r[17]), "=r"(r[18]), "=r"(r[19]), "=r"(r[20]), "=r"(r[21]), "=r"(r[22]), "=r"(r[23]),
-          "=r"(r[24]), "=r"(r[25]), "=r"(r[26]), "=r"(r[27]), "=r"(r[28]), "=r"(r[29]), "=r"(r[30]), "=r"(r[31])
-        : "r"(taddr));
-#pragma unroll
-    for (int i = 0; i < 32; ++i) v[i] = __uint_as_float(r[i]);
-}
+// 32 lanes x 16 columns of 32 bits: thread i gets columns c .. c + 15 of lane base + i
 __device__ __forceinline__ void ld16(uint32_t taddr, float *v) {
     uint32_t r[16];
     asm volatile(
@@ -104,12 +91,6 @@ __device__ __forceinline__ void tma_load_3d(uint32_t dst_smem, const CUtensorMap
         " [%0], [%1, {%2, %3, %4}], [%5];" ::"r"(dst_smem),
         "l"(reinterpret_cast<uint64_t>(map)), "r"(x), "r"(y), "r"(z), "r"(smem_u32(bar))
         : "memory");
-}
-// The same box into L2 only.
-__device__ __forceinline__ void tma_prefetch_3d(const CUtensorMap *map, int x, int y, int z) {
-    asm volatile("cp.async.bulk.prefetch.tensor.3d.L2.global.tile [%0, {%1, %2, %3}];" ::"l"(reinterpret_cast<uint64_t>(map)),
-                 "r"(x), "r"(y), "r"(z)
-                 : "memory");
 }
 __device__ __forceinline__ void prefetch_map(const CUtensorMap *map) {
     asm volatile("prefetch.tensormap [%0];" ::"l"(reinterpret_cast<uint64_t>(map)) : "memory");
