@@ -22,9 +22,10 @@
 // What bounds it.  d = 128: per 80-key tile of both streams the tensor core needs 1,490
 // clocks (measured alone; S with both operands in shared memory reads them at the
 // bank limit), the special-function units 1,280 for the exponentials; a step takes about
-// 1,850, and the clock is down to 1.56 GHz at the power limit.  2 x 8192 tokens, 64/8 heads: 1.75 ms,
-// 1,250 TFLOP/s; 16 x 1024 tokens, 32/8 heads: 0.17 ms, 815 TFLOP/s, where a job has 7 tiles and its
-// output rows (4,000 clocks) are no longer small beside them.
+// 1,850.  2 x 8192 tokens, 64/8 heads: 1.76 ms in a burst (1,225 TFLOP/s), 1.99 to 2.09 ms where
+// calls follow each other for 0.15 s and the power limit takes the clock down to 1.56 GHz; 16 x 1024 tokens,
+// 32/8 heads: 0.17 ms, 815 TFLOP/s, where a job has 7 tiles and its output rows (4,000 clocks) are no
+// longer small beside them.
 // d = 64: the products are half as long, the exponentials are not: 2,048 clocks of a step's 2,900.
 // Tried and slower: output rows written by four more warps (128 registers a thread at launch:
 // 184 us against 170 for 16 x 1024 tokens) or after the next job's first tile (189); jobs
@@ -51,8 +52,8 @@
 // survive: the loader zeroes the rows of the last tile that no row of the job sees, and a
 // row that comes out not finite while a value masked for it is not finite is
 // computed again (redo_rows).
-// Every wait is bounded; an abort drains the copies and MMAs in flight and frees the
-// tensor memory.
+// Every wait is bounded (from the last step of redo_rows, if there was one); an abort drains the
+// copies and MMAs in flight and frees the tensor memory.
 #include <cuda.h>
 #include <cudaTypedefs.h>
 
@@ -988,7 +989,7 @@ cudaError_t launch_prefill_packed(const PackedPrefill &a, cudaStream_t stream) {
     if (e != cudaSuccess) return e;
     // Where no sequence has more than one pair of row tiles, and a CTA at most kDirectJobs jobs,
     // the CTAs take (sequence, kv head) in turn and no list is made: without the first kernel 24
-    // prompts of up to 64 tokens take 11.6 us instead of 14.8, 40 of 200 to 256 tokens 26.3 instead of 29.2
+    // prompts of up to 64 tokens take 11.6 us instead of 14.8, 40 of 200 to 256 tokens 26.1 instead of 29.2
     // (1.3 and 2.2 jobs a CTA); with more jobs handing them out evens the CTAs (22 a CTA: 87 us
     // with the list, 89 without; 108: 392 and 416).
     const int64_t direct = (int64_t)a.num_seqs * a.num_kv_heads;

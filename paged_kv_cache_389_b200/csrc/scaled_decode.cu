@@ -530,8 +530,8 @@ __global__ void __launch_bounds__(kThreads, 1) decode_scaled_kernel(const __grid
     }
     const int64_t total = (int64_t)cum[ncum] * hkv;
     const int64_t workers = (int64_t)gridDim.x * kWarps;
-    // down to one item a warp: four sequences of 17 to 100 tokens take 7.9 us, with at least 2, 4, 8
-    // items 9.0, 9.9, 12.1
+    // down to one item a warp: four sequences of 17 to 100 tokens take 7.7 us (in a graph), with at
+    // least 2, 4, 8 items 9.0, 9.9, 12.1
     const int64_t per = (total + workers - 1) / workers;
     int64_t cta0 = min(total, (int64_t)blockIdx.x * kWarps * per), cta1 = min(total, cta0 + kWarps * per);
     int64_t warp_items = per;
@@ -773,7 +773,7 @@ cudaError_t launch(Params &p, void *workspace, int ctas, cudaStream_t stream) {
     cudaError_t e = cudaFuncSetAttribute(decode_scaled_kernel<D, G, kInt8>, cudaFuncAttributeMaxDynamicSharedMemorySize,
                                          (int)L::bytes(kMaxCum + 1));
     if (e != cudaSuccess) return e;
-    // Segments of at most kWholeItems items (496 tokens) stay within a CTA, which costs a CTA
+    // Segments of at most kWholeItems items (contexts of up to 511 tokens) stay within a CTA, which costs a CTA
     // at most one segment more than its share and saves the second kernel (four
     // sequences of 17 to 100 tokens: 9.1 us against 9.6 in a graph, at two items a warp).
     p.whole = p.max_context / kBlockSize + 2 <= kWholeItems;

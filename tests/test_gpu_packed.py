@@ -364,7 +364,7 @@ def test_rows_computed_again_take_as_long_as_they_take(pa, hq, hkv, d):
     clean, flag = run(pa, q, k, v, [0, T], 0.1)
     assert flag == 0
     v[-1] = float("nan")
-    pa.pa_set_wait_timeout_ns(300_000)
+    pa.pa_set_wait_timeout_ns(1_000_000)
     try:
         out, flag = run(pa, q, k, v, [0, T], 0.1)
     finally:
@@ -384,7 +384,7 @@ def test_rows_computed_again_take_as_long_as_they_take(pa, hq, hkv, d):
         bound = step_ops.attention_bound(p @ vv, p @ np.abs(vv), reach, (0, 2.0 ** -8, 0.0))
         assert (np.abs(f(out[T - n:T - 1, h]) - p @ vv) <= bound).all()
     v[:] = float("nan")
-    pa.pa_set_wait_timeout_ns(300_000)
+    pa.pa_set_wait_timeout_ns(1_000_000)
     try:
         out, flag = run(pa, q, k, v, [0, T], 0.1)
     finally:
