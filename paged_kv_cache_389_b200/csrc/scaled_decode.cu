@@ -250,7 +250,7 @@ __device__ __forceinline__ void block_step(unsigned char *stage, const float2 sc
     w[1] = pr[1] * f1;
     w[2] = pr[2] * f0;
     w[3] = pr[3] * f1;
-    // Where the factor is above 2^kFactor (block scales that far apart), a p of zero may stand for a w
+    // Where the factor is above kFactor (block scales that far apart), a p of zero may stand for a w
     // that is not: those blocks take the branch below, where w has an exponential of its own.
     const float a = fmax3(fmax3(pr[0], pr[1], pr[2]), pr[3], w[0]);
     const float b = fmax3(w[1], w[2], w[3]);
@@ -272,7 +272,7 @@ __device__ __forceinline__ void block_step(unsigned char *stage, const float2 sc
             x0 = fmaxf(x0, __shfl_xor_sync(kFull, x0, off));
             x1 = fmaxf(x1, __shfl_xor_sync(kFull, x1, off));
         }
-        const float log_v = __log2f(sc.y), lv = fmaxf(log_v, -100.f);   // m - mo stays within 2^107
+        const float log_v = __log2f(sc.y), lv = fmaxf(log_v, -100.f);   // m - mo is at most 100
         const float x[2] = {x0, x1};
         float ao[2];
 #pragma unroll
