@@ -390,3 +390,30 @@ def test_rows_computed_again_take_as_long_as_they_take(pa, hq, hkv, d):
     finally:
         pa.pa_set_wait_timeout_ns(0)
     assert flag == 0 and torch.isnan(out).all()
+
+
+@pytest.mark.gpu
+def test_offsets_beyond_32_bits(pa):
+    """Rows of one fused projection of more than 2^32 bytes (and an output of more), the last of 16,384
+    sequences at their end, a masked value that is not finite among them."""
+    torch = torch_mod()
+    hq, hkv, d, S = 64, 8, 128, 16384
+    rng = np.random.default_rng(14)
+    n = rng.integers(0, 3, S)
+    n[:8], n[-3:] = 35000, (257, 0, 140)
+    starts = np.concatenate([[0], np.cumsum(n)])
+    T = int(starts[-1]) + 5
+    assert T * hq * d * 2 > 2 ** 32
+    x = torch.zeros(T, hq + 2 * hkv, d, dtype=torch.bfloat16, device="cuda")
+    from_row = int(starts[-40])
+    x[from_row:] = bf16(rng.standard_normal((T - from_row, hq + 2 * hkv, d))).cuda()
+    q, k, v = x.split([hq, hkv, hkv], 1)
+    v[int(starts[-1]) - 1, :, 7] = float("inf")
+    out, flag = run(pa, q, k, v, starts, 0.09)
+    assert flag == 0 and (out[:35000:997] == 0).all()
+    tail = starts[-40:] - from_row
+    v[int(starts[-1]) - 1, :, 7] = 0
+    got = out[from_row:].clone()
+    assert torch.isinf(got[tail[-1] - 1, :, 7]).all()
+    got[tail[-1] - 1] = run(pa, q, k, v, starts, 0.09)[0][int(starts[-1]) - 1]
+    check(got, q[from_row:], k[from_row:], v[from_row:], tail, 0.09)

@@ -620,3 +620,38 @@ def test_decode_value_scales_at_both_ends_of_their_range(pa, code, d, low):
     bound = step_ops.attention_bound(ref, mass, reach, (0, 2.0 ** -11, 0.0)) + L * 2.0 ** -25 * top * step_ops.TOP[code]
     g = out.double().cpu().numpy()
     assert np.isfinite(g).all() and (np.abs(g - ref) <= bound).all()
+
+
+@pytest.mark.gpu
+@pytest.mark.parametrize("code", CODES)
+def test_append_of_rows_beyond_32_bits(pa, code):
+    """Rows of a fused projection of more than 2^32 bytes, the last tokens in blocks of their own (the
+    others are padding)."""
+    torch = torch_mod()
+    H, d, T, n = 8, 128, 240_000, 70
+    rng = np.random.default_rng(12)
+    x = torch.zeros(T, 10 * H, d, dtype=torch.bfloat16, device="cuda")
+    assert x.numel() * 2 > 2 ** 32
+    x[-n:] = bf16(rng.standard_normal((n, 10 * H, d))).cuda()
+    k, v = x[:, 8 * H:9 * H], x[:, 9 * H:]
+    kp, ks = random_pool(rng, 9, H, d, code)
+    slots = np.full(T, -1, np.int64)
+    slots[-n:] = appended(rng, 9, [5, 30], (20, 50))
+    got, flag = run_write(pa, k, v, slots, kp, kp, ks, ks, code)
+    assert flag == 0
+    want = [kp.copy(), kp.copy(), ks.copy(), ks.copy()]
+    for rows, i in ((k, 0), (v, 1)):
+        step_ops.cache_write_scaled(rows[-n:].double().cpu().numpy(), slots[-n:], want[i], want[2 + i], code)
+    assert all(same(g, w) for g, w in zip(got, want))
+
+
+@pytest.mark.gpu
+def test_decode_of_16384_sequences(pa):
+    """The most sequences a call takes, short and long contexts among them."""
+    rng = np.random.default_rng(16)
+    lens = rng.integers(0, 20, 16384)
+    lens[rng.integers(0, 16384, 30)] = rng.integers(500, 900, 30)
+    t = Decode(pa, "e4m3", 2, 1, 64, lens, seed=16)
+    t.call()
+    assert pa.pa_wait(t.err) == 0
+    t.check(np.concatenate([np.nonzero(lens > 100)[0], np.arange(40), rng.integers(0, 16384, 200), np.arange(16340, 16384)]))
